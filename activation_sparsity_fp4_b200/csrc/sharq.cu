@@ -13,11 +13,14 @@
 #include <string>
 
 #include "../../include/sharq.h"
+#include "fp4.cuh"
 #include "gemm.cuh"
+#include "gemm_fp4.cuh"
 #include "gemm_pair.cuh"
 #include "gemm_swap.cuh"
 #include "gemv.cuh"
 #include "prep.cuh"
+#include "route.cuh"
 
 using namespace sharq;
 
@@ -728,6 +731,164 @@ sharq_status run_linear(const sharq_prepared* a, const sharq_weight* w, const in
                 : launch_gemm_ws<GK_MXF4, false>(maps, gp, s, ws, ws_bytes);
 }
 
+// ------------------------------------------- plain FP4 layers and routing
+sharq_status check_fp4_shape(const sharq_fp4* a, const char* what) {
+  if (!a) return fail(SHARQ_ERR_INVALID, "%s: NULL", what);
+  if (a->fmt != SHARQ_MXFP4 && a->fmt != SHARQ_NVFP4) return fail(SHARQ_ERR_INVALID, "%s: bad format %d", what, (int)a->fmt);
+  if (a->k <= 0 || a->k % 32 != 0)
+    return fail(SHARQ_ERR_INVALID, "%s: k=%lld must be a positive multiple of 32", what, (long long)a->k);
+  if (a->rows <= 0) return fail(SHARQ_ERR_INVALID, "%s: rows=%lld must be positive", what, (long long)a->rows);
+  if (a->experts < 1) return fail(SHARQ_ERR_INVALID, "%s: experts=%d", what, (int)a->experts);
+  // rows and columns are 32-bit tensor coordinates
+  if (a->k > INT32_MAX / 2 || a->rows > (INT32_MAX - 256) / a->experts)
+    return fail(SHARQ_ERR_UNSUPPORTED, "%s: k=%lld or %d x %lld rows above the 32-bit coordinates", what, (long long)a->k,
+                (int)a->experts, (long long)a->rows);
+  return SHARQ_OK;
+}
+
+sharq_status check_fp4(const sharq_fp4* a, const char* what) {
+  sharq_status st = check_fp4_shape(a, what);
+  if (st != SHARQ_OK) return st;
+  const void* ptrs[3] = {a->codes, a->scales, a->row_scale};
+  for (int i = 0; i < 3; i++) {
+    if (!ptrs[i]) return fail(SHARQ_ERR_INVALID, "%s: buffer %d is NULL", what, i);
+    if (!aligned(ptrs[i], 16)) return fail(SHARQ_ERR_INVALID, "%s: buffer %d is not 16-byte aligned", what, i);
+  }
+  return SHARQ_OK;
+}
+
+sharq_status check_dtype(sharq_dtype dt, const char* what) {
+  if (dt != SHARQ_F32 && dt != SHARQ_BF16) return fail(SHARQ_ERR_INVALID, "bad %s dtype %d", what, (int)dt);
+  return SHARQ_OK;
+}
+
+// Input rows: 16-byte aligned, at least k values apart.
+sharq_status check_rows(const void* x, sharq_dtype dt, int64_t stride, int64_t k, const char* what) {
+  if (!x || !aligned(x, 16)) return fail(SHARQ_ERR_INVALID, "%s must be a 16-byte aligned device pointer", what);
+  const int64_t per16 = dt == SHARQ_BF16 ? 8 : 4;
+  if (stride < k || stride % per16 != 0)
+    return fail(SHARQ_ERR_INVALID, "%s: row stride %lld must be at least %lld and a multiple of 16 bytes", what,
+                (long long)stride, (long long)k);
+  return SHARQ_OK;
+}
+
+template <int FMT, int FRONT, bool XBF16>
+sharq_status launch_fp4(const Fp4Params& fp, cudaStream_t s) {
+  return launch_ex(fp4_kernel<FMT, FRONT, XBF16>, dim3((unsigned)fp.rows_out), dim3(128), 0, s, 1, fp);
+}
+template <int FRONT>
+sharq_status fp4_dispatch(const Fp4Params& fp, sharq_format fmt, bool bf16, cudaStream_t s) {
+  if (fmt == SHARQ_NVFP4) return bf16 ? launch_fp4<FMT_NV, FRONT, true>(fp, s) : launch_fp4<FMT_NV, FRONT, false>(fp, s);
+  return bf16 ? launch_fp4<FMT_MX, FRONT, true>(fp, s) : launch_fp4<FMT_MX, FRONT, false>(fp, s);
+}
+
+Fp4Params fp4_params(const void* x, int64_t x_rows, int64_t stride, const int32_t* count, float amax,
+                     const sharq_fp4* out) {
+  Fp4Params fp;
+  memset(&fp, 0, sizeof(fp));
+  fp.x = x;
+  fp.x_rows = x_rows;
+  fp.stride = stride;
+  fp.count = count;
+  fp.amax = amax > 0.0f ? amax : 0.0f;
+  fp.rows_out = out->rows * out->experts;
+  fp.rows_expert = out->rows;
+  fp.k = out->k;
+  fp.codes = static_cast<uint8_t*>(out->codes);
+  fp.scales = static_cast<uint8_t*>(out->scales);
+  fp.row_scale = out->row_scale;
+  return fp;
+}
+
+template <int KIND, int CTAS, bool GROUPED>
+sharq_status launch_gemm_fp4(const sharq_fp4* x, const sharq_fp4* w, const int32_t* offsets, void* y, sharq_dtype y_dt,
+                             cudaStream_t s) {
+  using C = Fp4Cfg<KIND, CTAS>;
+  sharq_status st = ensure_smem_limit<gemm_fp4_kernel<KIND, CTAS, GROUPED>>(C::kSmemBytes);
+  if (st != SHARQ_OK) return st;
+  const int64_t t = x->rows, n = w->rows, k = x->k, es = y_dt == SHARQ_BF16 ? 2 : 4;
+  Fp4Maps maps;
+  memset(&maps, 0, sizeof(maps));
+  st = make_map(&maps.x, x->codes, k / 2, t, 128, C::BM, CU_TENSOR_MAP_SWIZZLE_128B);
+  if (st != SHARQ_OK) return st;
+  st = make_map(&maps.w, w->codes, k / 2, n * w->experts, 128, C::BNh, CU_TENSOR_MAP_SWIZZLE_128B);
+  if (st != SHARQ_OK) return st;
+  st = make_map(&maps.y, y, n * es, t, C::kYRow, 32, CU_TENSOR_MAP_SWIZZLE_NONE);
+  if (st != SHARQ_OK) return st;
+  Fp4GemmParams gp;
+  memset(&gp, 0, sizeof(gp));
+  gp.t = t;
+  gp.n = n;
+  gp.k = k;
+  gp.experts = w->experts;
+  gp.group_offsets = offsets;
+  gp.sf_x = static_cast<const uint8_t*>(x->scales);
+  gp.sf_w = static_cast<const uint8_t*>(w->scales);
+  gp.row_x = x->row_scale;
+  gp.row_w = w->row_scale;
+  gp.y_bf16 = y_dt == SHARQ_BF16;
+  gp.timeout_ns = wait_timeout_ns();
+  const int64_t tiles = ((t + C::BM * CTAS - 1) / (C::BM * CTAS)) * ((n + C::BN - 1) / C::BN);
+  if (tiles > INT32_MAX / 2) return fail(SHARQ_ERR_UNSUPPORTED, "%lld output tiles", (long long)tiles);
+  const int64_t slots = sm_count() / CTAS;
+  return launch_ex(gemm_fp4_kernel<KIND, CTAS, GROUPED>, dim3((unsigned)(CTAS * (tiles < slots ? tiles : slots))), dim3(448),
+                   C::kSmemBytes, s, CTAS, maps, gp);
+}
+
+sharq_status run_linear_fp4(const sharq_fp4* x, const sharq_fp4* w, const int32_t* offsets, void* y, sharq_dtype y_dt,
+                            cudaStream_t s) {
+  sharq_status st = check_fp4(x, "activations");
+  if (st != SHARQ_OK) return st;
+  st = check_fp4(w, "weight");
+  if (st != SHARQ_OK) return st;
+  if (x->k != w->k)
+    return fail(SHARQ_ERR_INVALID, "k mismatch: activations %lld, weight %lld", (long long)x->k, (long long)w->k);
+  if (x->fmt != w->fmt) return fail(SHARQ_ERR_INVALID, "format mismatch between activations and weight");
+  if (x->experts != 1) return fail(SHARQ_ERR_INVALID, "activations with experts=%d", (int)x->experts);
+  if (!offsets && w->experts != 1) return fail(SHARQ_ERR_INVALID, "a stacked weight needs sharq_linear_fp4_grouped");
+  if (w->rows % 8 != 0) return fail(SHARQ_ERR_INVALID, "n=%lld must be a multiple of 8", (long long)w->rows);
+  if (w->rows > INT32_MAX / 4) return fail(SHARQ_ERR_UNSUPPORTED, "n=%lld above the 32-bit coordinates", (long long)w->rows);
+  if (!y || !aligned(y, 16)) return fail(SHARQ_ERR_INVALID, "y must be a 16-byte aligned device pointer");
+  st = check_dtype(y_dt, "y");
+  if (st != SHARQ_OK) return st;
+  if (offsets)
+    return x->fmt == SHARQ_NVFP4 ? launch_gemm_fp4<GK_NVF4, 1, true>(x, w, offsets, y, y_dt, s)
+                                 : launch_gemm_fp4<GK_MXF4, 1, true>(x, w, offsets, y, y_dt, s);
+  return x->fmt == SHARQ_NVFP4 ? launch_gemm_fp4<GK_NVF4, 1, false>(x, w, nullptr, y, y_dt, s)
+                               : launch_gemm_fp4<GK_MXF4, 1, false>(x, w, nullptr, y, y_dt, s);
+}
+
+template <int VPL>
+sharq_status launch_route(const RouteParams& rp, bool bf16, cudaStream_t s) {
+  const size_t smem = rp.groups > 1 ? 4 * (size_t)rp.experts * sizeof(double) : 0;
+  const dim3 grid((unsigned)((rp.t + 3) / 4));
+  return bf16 ? launch_ex(route_kernel<VPL, true>, grid, dim3(128), smem, s, 1, rp)
+              : launch_ex(route_kernel<VPL, false>, grid, dim3(128), smem, s, 1, rp);
+}
+
+sharq_status check_assignment(int64_t t, int32_t top_k, int32_t experts) {
+  if (t <= 0) return fail(SHARQ_ERR_INVALID, "t=%lld must be positive", (long long)t);
+  if (experts < 1) return fail(SHARQ_ERR_INVALID, "experts=%d must be positive", (int)experts);
+  if (experts > kMaxExperts) return fail(SHARQ_ERR_UNSUPPORTED, "experts=%d above %d", (int)experts, kMaxExperts);
+  if (top_k < 1) return fail(SHARQ_ERR_INVALID, "top_k=%d must be positive", (int)top_k);
+  if (top_k > kMaxTopK) return fail(SHARQ_ERR_UNSUPPORTED, "top_k=%d above %d", (int)top_k, kMaxTopK);
+  // row numbers are 32-bit
+  if (t > (INT32_MAX - 128 * kMaxExperts) / top_k) return fail(SHARQ_ERR_UNSUPPORTED, "t=%lld tokens", (long long)t);
+  return SHARQ_OK;
+}
+
+int64_t rows_capacity(int64_t t, int32_t top_k, int32_t experts) {
+  const int64_t n = t * top_k, reached = n < experts ? n : experts;
+  return 128 * (reached + (n - reached) / 128);
+}
+
+template <bool YBF16, bool OBF16>
+sharq_status launch_combine(const CombineParams& cp, cudaStream_t s) {
+  const int64_t blocks = (cp.t * (cp.n / 8) + 127) / 128;
+  if (blocks > INT32_MAX) return fail(SHARQ_ERR_UNSUPPORTED, "t=%lld, n=%lld", (long long)cp.t, (long long)cp.n);
+  return launch_ex(combine_kernel<YBF16, OBF16>, dim3((unsigned)blocks), dim3(128), 0, s, 1, cp);
+}
+
 }  // namespace
 
 // Scratch of sharq_prepare_noalloc: one float (a row's RMSNorm factor) per row
@@ -1087,6 +1248,182 @@ sharq_status sharq_linear_grouped_gather(const sharq_prepared* tokens, const int
   gp.g_bb_codes = static_cast<const uint8_t*>(tokens->bb_codes);
   gp.g_meta = static_cast<const uint8_t*>(tokens->meta);
   return launch_gemm<GK_NVF4, true, false, true>(maps, gp, s);
+}
+
+sharq_status sharq_fp4_sizes(int64_t rows, int64_t k, int32_t experts, sharq_format fmt, size_t* codes_bytes,
+                             size_t* scales_bytes, size_t* row_scale_bytes) {
+  const sharq_fp4 a = {nullptr, nullptr, nullptr, rows, k, experts, fmt};
+  sharq_status st = check_fp4_shape(&a, "sizes");
+  if (st != SHARQ_OK) return st;
+  if (codes_bytes) *codes_bytes = (size_t)experts * rows * (k / 2);
+  if (scales_bytes) *scales_bytes = (size_t)experts * tiled_sf_bytes(rows, k / fmt_block(fmt));
+  if (row_scale_bytes) *row_scale_bytes = (size_t)experts * rows * sizeof(float);
+  return SHARQ_OK;
+}
+
+sharq_status sharq_quantize_fp4(const void* x, sharq_dtype x_dt, int64_t x_rows, int64_t x_stride,
+                                const int32_t* rows, const int32_t* count, const void* gamma, float eps, float amax,
+                                sharq_fp4* out, sharq_stream stream) {
+  sharq_status st = check_fp4(out, "out");
+  if (st != SHARQ_OK) return st;
+  st = check_dtype(x_dt, "x");
+  if (st != SHARQ_OK) return st;
+  st = check_rows(x, x_dt, x_stride, out->k, "x");
+  if (st != SHARQ_OK) return st;
+  if (x_rows <= 0) return fail(SHARQ_ERR_INVALID, "x_rows=%lld must be positive", (long long)x_rows);
+  if (!rows && x_rows != out->rows * out->experts)
+    return fail(SHARQ_ERR_INVALID, "x has %lld rows, out %lld", (long long)x_rows, (long long)(out->rows * out->experts));
+  if ((rows || count) && out->experts != 1) return fail(SHARQ_ERR_INVALID, "rows and count need experts=1");
+  if (!aligned(rows, 4) || !aligned(count, 4)) return fail(SHARQ_ERR_INVALID, "rows and count must be device int32 arrays");
+  if (gamma && !aligned(gamma, 16)) return fail(SHARQ_ERR_INVALID, "gamma must be 16-byte aligned");
+  if (!(eps >= 0.0f)) return fail(SHARQ_ERR_INVALID, "eps must be >= 0");
+  Fp4Params fp = fp4_params(x, x_rows, x_stride, count, amax, out);
+  fp.rows = rows;
+  fp.gamma = gamma;
+  fp.eps = eps;
+  cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
+  const bool bf16 = x_dt == SHARQ_BF16;
+  return gamma ? fp4_dispatch<FRONT_NORM>(fp, out->fmt, bf16, s) : fp4_dispatch<FRONT_NONE>(fp, out->fmt, bf16, s);
+}
+
+sharq_status sharq_quantize_fp4_swiglu(const void* gate, const void* up, sharq_dtype dt, int64_t stride,
+                                       const int32_t* count, float amax, sharq_fp4* out, sharq_stream stream) {
+  sharq_status st = check_fp4(out, "out");
+  if (st != SHARQ_OK) return st;
+  st = check_dtype(dt, "gate and up");
+  if (st != SHARQ_OK) return st;
+  st = check_rows(gate, dt, stride, out->k, "gate");
+  if (st != SHARQ_OK) return st;
+  st = check_rows(up, dt, stride, out->k, "up");
+  if (st != SHARQ_OK) return st;
+  if (out->experts != 1) return fail(SHARQ_ERR_INVALID, "activations with experts=%d", (int)out->experts);
+  if (!aligned(count, 4)) return fail(SHARQ_ERR_INVALID, "count must be a device int32");
+  Fp4Params fp = fp4_params(gate, out->rows, stride, count, amax, out);
+  fp.x2 = up;
+  return fp4_dispatch<FRONT_SWIGLU>(fp, out->fmt, dt == SHARQ_BF16, reinterpret_cast<cudaStream_t>(stream));
+}
+
+sharq_status sharq_linear_fp4(const sharq_fp4* x, const sharq_fp4* w, void* y, sharq_dtype y_dt, sharq_stream stream) {
+  return run_linear_fp4(x, w, nullptr, y, y_dt, reinterpret_cast<cudaStream_t>(stream));
+}
+
+sharq_status sharq_linear_fp4_grouped(const sharq_fp4* x, const sharq_fp4* w, const int32_t* group_offsets, void* y,
+                                      sharq_dtype y_dt, sharq_stream stream) {
+  if (!group_offsets || !aligned(group_offsets, 4))
+    return fail(SHARQ_ERR_INVALID, "group_offsets must be a device int32 array");
+  return run_linear_fp4(x, w, group_offsets, y, y_dt, reinterpret_cast<cudaStream_t>(stream));
+}
+
+sharq_status sharq_route(const void* logits, sharq_dtype dt, int64_t t, int32_t experts, int64_t stride,
+                         const float* bias, sharq_score score, int32_t groups, int32_t top_groups, int32_t group_top,
+                         int32_t top_k, int32_t renormalize, float scale, int32_t* ids, float* weights,
+                         sharq_stream stream) {
+  sharq_status st = check_assignment(t, top_k, experts);
+  if (st != SHARQ_OK) return st;
+  st = check_dtype(dt, "logits");
+  if (st != SHARQ_OK) return st;
+  if (!logits || !aligned(logits, dt == SHARQ_BF16 ? 2 : 4)) return fail(SHARQ_ERR_INVALID, "logits must be an aligned device pointer");
+  if (stride < experts) return fail(SHARQ_ERR_INVALID, "row stride %lld below experts=%d", (long long)stride, (int)experts);
+  if (!aligned(bias, 4)) return fail(SHARQ_ERR_INVALID, "bias must be a device float array");
+  if (score != SHARQ_SOFTMAX && score != SHARQ_SIGMOID) return fail(SHARQ_ERR_INVALID, "bad score %d", (int)score);
+  if (groups < 1 || experts % groups != 0)
+    return fail(SHARQ_ERR_INVALID, "groups=%d must divide experts=%d", (int)groups, (int)experts);
+  if (groups > kMaxGroups) return fail(SHARQ_ERR_UNSUPPORTED, "groups=%d above %d", (int)groups, kMaxGroups);
+  if (top_groups < 1 || top_groups > groups) return fail(SHARQ_ERR_INVALID, "top_groups=%d of %d", (int)top_groups, (int)groups);
+  if (group_top < 1 || group_top > 2) return fail(SHARQ_ERR_INVALID, "group_top=%d must be 1 or 2", (int)group_top);
+  if (top_k > top_groups * (experts / groups))
+    return fail(SHARQ_ERR_INVALID, "top_k=%d above the %d experts of top_groups", (int)top_k, (int)(top_groups * (experts / groups)));
+  if (!ids || !aligned(ids, 4) || !weights || !aligned(weights, 4))
+    return fail(SHARQ_ERR_INVALID, "ids and weights must be device arrays");
+  RouteParams rp;
+  rp.logits = logits;
+  rp.t = t;
+  rp.stride = stride;
+  rp.bias = bias;
+  rp.experts = experts;
+  rp.groups = groups;
+  rp.top_groups = top_groups;
+  rp.group_top = group_top;
+  rp.top_k = top_k;
+  rp.softmax = score == SHARQ_SOFTMAX;
+  rp.renormalize = renormalize != 0;
+  rp.scale = scale;
+  rp.ids = ids;
+  rp.weights = weights;
+  cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
+  const bool bf16 = dt == SHARQ_BF16;
+  if (experts <= 32) return launch_route<1>(rp, bf16, s);
+  if (experts <= 64) return launch_route<2>(rp, bf16, s);
+  if (experts <= 128) return launch_route<4>(rp, bf16, s);
+  if (experts <= 256) return launch_route<8>(rp, bf16, s);
+  return launch_route<16>(rp, bf16, s);
+}
+
+sharq_status sharq_route_rows_capacity(int64_t t, int32_t top_k, int32_t experts, int64_t* capacity) {
+  sharq_status st = check_assignment(t, top_k, experts);
+  if (st != SHARQ_OK) return st;
+  if (!capacity) return fail(SHARQ_ERR_INVALID, "capacity is NULL");
+  *capacity = rows_capacity(t, top_k, experts);
+  return SHARQ_OK;
+}
+
+sharq_status sharq_route_rows(const int32_t* ids, int64_t t, int32_t top_k, int32_t experts, int32_t* rows,
+                              int64_t capacity, int32_t* group_offsets, int32_t* slots, sharq_stream stream) {
+  sharq_status st = check_assignment(t, top_k, experts);
+  if (st != SHARQ_OK) return st;
+  const void* ptrs[4] = {ids, rows, group_offsets, slots};
+  for (int i = 0; i < 4; i++)
+    if (!ptrs[i] || !aligned(ptrs[i], 4)) return fail(SHARQ_ERR_INVALID, "array %d must be a device int32 array", i);
+  if (capacity < rows_capacity(t, top_k, experts))
+    return fail(SHARQ_ERR_WORKSPACE, "capacity %lld below the %lld rows this assignment may need", (long long)capacity,
+                (long long)rows_capacity(t, top_k, experts));
+  RowsParams rp;
+  rp.ids = ids;
+  rp.n = t * top_k;
+  rp.top_k = top_k;
+  rp.experts = experts;
+  rp.rows = rows;
+  rp.capacity = capacity;
+  rp.offsets = group_offsets;
+  rp.slots = slots;
+  const int max_smem = (int)sizeof(int32_t) * ((kRowsWarps + 3) * kMaxExperts + 1);
+  st = ensure_smem_limit<route_rows_kernel>(max_smem);
+  if (st != SHARQ_OK) return st;
+  const int64_t want = (rp.n + 1023) / 1024;  // a step of every warp of a CTA takes 1024 ids
+  const unsigned ctas = want >= 8 ? 8 : want >= 4 ? 4 : want >= 2 ? 2 : 1;
+  const size_t smem = sizeof(int32_t) * ((kRowsWarps + 3) * (size_t)experts + 1);
+  return launch_ex(route_rows_kernel, dim3(ctas), dim3(kRowsWarps * 32), smem, reinterpret_cast<cudaStream_t>(stream), ctas, rp);
+}
+
+sharq_status sharq_combine(const void* y, sharq_dtype y_dt, int64_t y_rows, int64_t n, const int32_t* slots,
+                           const float* weights, int64_t t, int32_t top_k, const void* add, void* out,
+                           sharq_dtype out_dt, sharq_stream stream) {
+  sharq_status st = check_assignment(t, top_k, 1);
+  if (st != SHARQ_OK) return st;
+  st = check_dtype(y_dt, "y");
+  if (st != SHARQ_OK) return st;
+  st = check_dtype(out_dt, "out");
+  if (st != SHARQ_OK) return st;
+  if (y_rows <= 0) return fail(SHARQ_ERR_INVALID, "y_rows=%lld must be positive", (long long)y_rows);
+  if (n <= 0 || n % 8 != 0) return fail(SHARQ_ERR_INVALID, "n=%lld must be a positive multiple of 8", (long long)n);
+  if (!y || !aligned(y, 16) || !aligned(add, 16) || !out || !aligned(out, 16))
+    return fail(SHARQ_ERR_INVALID, "y, add and out must be 16-byte aligned device pointers");
+  if (!slots || !aligned(slots, 4) || !weights || !aligned(weights, 4))
+    return fail(SHARQ_ERR_INVALID, "slots and weights must be device arrays");
+  CombineParams cp;
+  cp.y = y;
+  cp.y_rows = y_rows;
+  cp.n = n;
+  cp.slots = slots;
+  cp.weights = weights;
+  cp.t = t;
+  cp.top_k = top_k;
+  cp.add = add;
+  cp.out = out;
+  cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
+  if (y_dt == SHARQ_BF16)
+    return out_dt == SHARQ_BF16 ? launch_combine<true, true>(cp, s) : launch_combine<true, false>(cp, s);
+  return out_dt == SHARQ_BF16 ? launch_combine<false, true>(cp, s) : launch_combine<false, false>(cp, s);
 }
 
 sharq_status sharq_sync_status(sharq_stream stream) {

@@ -8,8 +8,10 @@ There is no CPU fallback: without the built library every call raises.
 """
 from __future__ import annotations
 
+import contextlib
 import ctypes
 import os
+from typing import NamedTuple
 
 import torch
 
@@ -19,6 +21,7 @@ MXFP4, NVFP4 = 0, 1
 NM_2_4, NM_4_8_PAIR, NM_8_16, NM_8_16_PAIR = 0, 1, 2, 3
 F32, BF16 = 0, 1
 FORMATS = {"mxfp4": MXFP4, "nvfp4": NVFP4}
+SCORES = {"softmax": 0, "sigmoid": 1}
 PATTERNS = {"2:4": NM_2_4, "4:8pair": NM_4_8_PAIR, "8:16": NM_8_16, "8:16pair": NM_8_16_PAIR}
 STATUS = {0: "SHARQ_OK", 1: "SHARQ_ERR_INVALID", 2: "SHARQ_ERR_UNSUPPORTED", 3: "SHARQ_ERR_CUDA",
           4: "SHARQ_ERR_TIMEOUT", 5: "SHARQ_ERR_WORKSPACE"}
@@ -26,7 +29,9 @@ SYMBOLS = ["sharq_weight_sizes", "sharq_prepared_sizes", "sharq_quantize_weight"
            "sharq_linear_paths", "sharq_linear_grouped", "sharq_sync_status", "sharq_selftest_wait_timeout",
            "sharq_last_error", "sharq_launch_count", "sharq_prepare_noalloc", "sharq_prepare_swiglu",
            "sharq_gather_prepared", "sharq_linear_ws", "sharq_linear_workspace_size",
-           "sharq_linear_grouped_gather"]
+           "sharq_linear_grouped_gather", "sharq_fp4_sizes", "sharq_quantize_fp4", "sharq_quantize_fp4_swiglu",
+           "sharq_linear_fp4", "sharq_linear_fp4_grouped", "sharq_route", "sharq_route_rows_capacity",
+           "sharq_route_rows", "sharq_combine"]
 NOALLOC_MAX_ROWS = 65536  # SHARQ_NOALLOC_MAX_ROWS of the C header
 
 
@@ -46,6 +51,11 @@ class sharq_prepared(ctypes.Structure):
     _fields_ = [("meta", ctypes.c_void_p), ("bb_codes", ctypes.c_void_p), ("bb_scales", ctypes.c_void_p),
                 ("res_codes", ctypes.c_void_p), ("res_scales", ctypes.c_void_p), ("tensor", ctypes.c_void_p),
                 ("t", ctypes.c_int64), ("k", ctypes.c_int64), ("fmt", ctypes.c_int), ("pat", ctypes.c_int)]
+
+
+class sharq_fp4(ctypes.Structure):
+    _fields_ = [("codes", ctypes.c_void_p), ("scales", ctypes.c_void_p), ("row_scale", ctypes.c_void_p),
+                ("rows", ctypes.c_int64), ("k", ctypes.c_int64), ("experts", ctypes.c_int32), ("fmt", ctypes.c_int)]
 
 
 _lib = None
@@ -82,6 +92,15 @@ def lib() -> ctypes.CDLL:
             "sharq_linear_grouped": [ctypes.POINTER(sharq_prepared), ctypes.POINTER(sharq_weight), P, P, I, P],
             "sharq_linear_grouped_gather": [ctypes.POINTER(sharq_prepared), P, I64, ctypes.POINTER(sharq_weight), P,
                                             P, I, P],
+            "sharq_fp4_sizes": [I64, I64, I32, I, SZ, SZ, SZ],
+            "sharq_quantize_fp4": [P, I, I64, I64, P, P, P, F, F, ctypes.POINTER(sharq_fp4), P],
+            "sharq_quantize_fp4_swiglu": [P, P, I, I64, P, F, ctypes.POINTER(sharq_fp4), P],
+            "sharq_linear_fp4": [ctypes.POINTER(sharq_fp4), ctypes.POINTER(sharq_fp4), P, I, P],
+            "sharq_linear_fp4_grouped": [ctypes.POINTER(sharq_fp4), ctypes.POINTER(sharq_fp4), P, P, I, P],
+            "sharq_route": [P, I, I64, I32, I64, P, I, I32, I32, I32, I32, I32, F, P, P, P],
+            "sharq_route_rows_capacity": [I64, I32, I32, ctypes.POINTER(I64)],
+            "sharq_route_rows": [P, I64, I32, I32, P, I64, P, P, P],
+            "sharq_combine": [P, I, I64, I64, P, P, I64, I32, P, P, I, P],
             "sharq_sync_status": [P],
             "sharq_selftest_wait_timeout": [ctypes.c_uint64, P],
         }
@@ -110,6 +129,10 @@ def _stream(stream=None):
 
 def _fmt(f) -> int:
     return FORMATS[f] if isinstance(f, str) else int(f)
+
+
+def _score(v) -> int:
+    return SCORES[v] if isinstance(v, str) else int(v)
 
 
 def _pat(p) -> int:
@@ -205,6 +228,60 @@ def sharq_linear_grouped_gather(tokens: sharq_prepared, rows_ptr: int, routed_ro
     _check(lib().sharq_linear_grouped_gather(ctypes.byref(tokens), ctypes.c_void_p(rows_ptr), int(routed_rows),
                                              ctypes.byref(w), ctypes.c_void_p(offsets_ptr), ctypes.c_void_p(y_ptr),
                                              _dt(y_dt), _stream(stream)), "sharq_linear_grouped_gather")
+
+
+def sharq_fp4_sizes(rows: int, k: int, experts: int, fmt) -> tuple[int, int, int]:
+    out = [ctypes.c_size_t() for _ in range(3)]
+    _check(lib().sharq_fp4_sizes(rows, k, experts, _fmt(fmt), *[ctypes.byref(o) for o in out]), "sharq_fp4_sizes")
+    return tuple(o.value for o in out)
+
+
+def sharq_quantize_fp4(x_ptr: int, x_dt, x_rows: int, x_stride: int, rows_ptr, count_ptr, gamma_ptr, eps: float,
+                       amax: float, out: sharq_fp4, stream=None):
+    _check(lib().sharq_quantize_fp4(x_ptr, _dt(x_dt), x_rows, x_stride, rows_ptr, count_ptr, gamma_ptr, eps, amax,
+                                    ctypes.byref(out), _stream(stream)), "sharq_quantize_fp4")
+
+
+def sharq_quantize_fp4_swiglu(gate_ptr: int, up_ptr: int, dt, stride: int, count_ptr, amax: float, out: sharq_fp4,
+                              stream=None):
+    _check(lib().sharq_quantize_fp4_swiglu(gate_ptr, up_ptr, _dt(dt), stride, count_ptr, amax, ctypes.byref(out),
+                                           _stream(stream)), "sharq_quantize_fp4_swiglu")
+
+
+def sharq_linear_fp4(x: sharq_fp4, w: sharq_fp4, y_ptr: int, y_dt, stream=None):
+    _check(lib().sharq_linear_fp4(ctypes.byref(x), ctypes.byref(w), y_ptr, _dt(y_dt), _stream(stream)),
+           "sharq_linear_fp4")
+
+
+def sharq_linear_fp4_grouped(x: sharq_fp4, w: sharq_fp4, offsets_ptr: int, y_ptr: int, y_dt, stream=None):
+    _check(lib().sharq_linear_fp4_grouped(ctypes.byref(x), ctypes.byref(w), offsets_ptr, y_ptr, _dt(y_dt),
+                                          _stream(stream)), "sharq_linear_fp4_grouped")
+
+
+def sharq_route(logits_ptr: int, dt, t: int, experts: int, stride: int, bias_ptr, score, groups: int, top_groups: int,
+                group_top: int, top_k: int, renormalize: bool, scale: float, ids_ptr: int, weights_ptr: int,
+                stream=None):
+    _check(lib().sharq_route(logits_ptr, _dt(dt), t, experts, stride, bias_ptr, _score(score), groups, top_groups,
+                             group_top, top_k, 1 if renormalize else 0, scale, ids_ptr, weights_ptr, _stream(stream)),
+           "sharq_route")
+
+
+def sharq_route_rows_capacity(t: int, top_k: int, experts: int) -> int:
+    out = ctypes.c_int64(0)
+    _check(lib().sharq_route_rows_capacity(t, top_k, experts, ctypes.byref(out)), "sharq_route_rows_capacity")
+    return int(out.value)
+
+
+def sharq_route_rows(ids_ptr: int, t: int, top_k: int, experts: int, rows_ptr: int, capacity: int, offsets_ptr: int,
+                     slots_ptr: int, stream=None):
+    _check(lib().sharq_route_rows(ids_ptr, t, top_k, experts, rows_ptr, capacity, offsets_ptr, slots_ptr,
+                                  _stream(stream)), "sharq_route_rows")
+
+
+def sharq_combine(y_ptr: int, y_dt, y_rows: int, n: int, slots_ptr: int, weights_ptr: int, t: int, top_k: int, add_ptr,
+                  out_ptr: int, out_dt, stream=None):
+    _check(lib().sharq_combine(y_ptr, _dt(y_dt), y_rows, n, slots_ptr, weights_ptr, t, top_k, add_ptr, out_ptr,
+                               _dt(out_dt), _stream(stream)), "sharq_combine")
 
 
 def sharq_sync_status(stream=None):
@@ -353,4 +430,230 @@ def linear_grouped_gather(tokens: Prepared, rows: torch.Tensor, w: FP4Weight, of
     offsets = offsets.to(torch.int32).contiguous()
     sharq_linear_grouped_gather(tokens.struct, rows.data_ptr(), rows.numel(), w.struct, offsets.data_ptr(),
                                 out.data_ptr(), out.dtype, stream)
+    return out
+
+
+# ------------------------------------- plain FP4 layers and expert routing
+@contextlib.contextmanager
+def _on(x: torch.Tensor, stream):
+    """Allocate and launch where x lives: its device, and the given stream (default: that device's current one)."""
+    if not x.is_cuda:
+        raise ValueError("a CUDA tensor is needed")
+    with torch.cuda.device(x.device), torch.cuda.stream(stream):
+        yield
+
+
+def _place(x: torch.Tensor, stream):
+    # the usual call, on the current device's current stream, needs no context at all
+    if stream is None and x.is_cuda and x.device.index == torch.cuda.current_device():
+        return contextlib.nullcontext()
+    if isinstance(stream, int):
+        stream = torch.cuda.ExternalStream(stream, device=x.device)
+    return _on(x, stream)
+
+
+def _same_device(x: torch.Tensor, **others):
+    for name, o in others.items():
+        if o is not None and o.device != x.device:
+            raise ValueError(f"{name} is on {o.device}, the call's first tensor on {x.device}")
+
+
+def _rows_of(x: torch.Tensor, what: str) -> torch.Tensor:
+    """x as rows of adjacent values whose starts are 16-byte aligned (a copy only where it is not so already)."""
+    if x.dim() != 2:
+        raise ValueError(f"{what} must have two dimensions, has {x.dim()}")
+    size = x.element_size()
+    if x.stride(1) != 1 or x.stride(0) < x.shape[1] or (x.stride(0) * size) % 16 or x.data_ptr() % 16:
+        x = x.clone(memory_format=torch.contiguous_format)
+    return x
+
+
+def _i32(x: torch.Tensor, what: str, shape=None) -> torch.Tensor:
+    if x.dtype != torch.int32:
+        raise ValueError(f"{what} must be int32, is {x.dtype}")
+    if shape is not None and tuple(x.shape) != tuple(shape):
+        raise ValueError(f"{what} must have shape {tuple(shape)}, has {tuple(x.shape)}")
+    return x.contiguous()
+
+
+def _ptr(x: torch.Tensor | None):
+    return None if x is None else x.data_ptr()
+
+
+class FP4Matrix:
+    """Device buffers of a microscaled FP4 matrix: activations, or a weight of one or ``experts`` stacked blocks."""
+
+    def __init__(self, rows: int, k: int, fmt, experts: int = 1, device="cuda"):
+        self.rows, self.k, self.fmt, self.experts = rows, k, _fmt(fmt), experts
+        c, s, r = sharq_fp4_sizes(rows, k, experts, self.fmt)
+        self.codes = _alloc(c, device)
+        self.scales = _alloc(s, device)
+        self.row_scale = torch.empty(experts * rows, dtype=torch.float32, device=device)
+        self.struct = sharq_fp4(self.codes.data_ptr(), self.scales.data_ptr(), self.row_scale.data_ptr(), rows, k,
+                                experts, self.fmt)
+
+    @property
+    def device(self):
+        return self.codes.device
+
+
+def _fp4_out(out: FP4Matrix | None, rows: int, k: int, fmt, experts: int, x: torch.Tensor) -> FP4Matrix:
+    if out is None:
+        return FP4Matrix(rows, k, fmt, experts, x.device)
+    if (out.rows, out.k, out.fmt, out.experts, out.device) != (rows, k, _fmt(fmt), experts, x.device):
+        raise ValueError("out does not fit: another shape, format or device")
+    return out
+
+
+def quantize_fp4(x: torch.Tensor, fmt, rows: torch.Tensor | None = None, gamma: torch.Tensor | None = None,
+                 eps: float = 1e-6, amax: float = 0.0, count: torch.Tensor | None = None,
+                 out: FP4Matrix | None = None, stream=None) -> FP4Matrix:
+    """Rows of x as an FP4 matrix: x (t, k), or (experts, n, k) for a stacked weight.
+    rows: int32 indexes of the rows to take (out of range: a zero row).  gamma: RMSNorm
+    in front.  count: one int32 on the GPU; rows from it on are left as they were."""
+    if x.dim() not in (2, 3):
+        raise ValueError(f"x must be (t, k) or (experts, n, k), has {x.dim()} dimensions")
+    _same_device(x, rows=rows, gamma=gamma, count=count)
+    with _place(x, stream):
+        experts = x.shape[0] if x.dim() == 3 else 1
+        x2 = _rows_of(x if x.dim() == 2 else x.flatten(0, 1), "x")
+        if gamma is not None:
+            if tuple(gamma.shape) != (x2.shape[1],):
+                raise ValueError(f"gamma must have shape ({x2.shape[1]},)")
+            gamma = _aligned(gamma.to(x.dtype))
+        if rows is not None:
+            rows = _i32(rows, "rows", (rows.numel(),))
+        if count is not None:
+            count = _i32(count, "count", (1,))
+        n_rows = x.shape[-2] if rows is None else rows.numel()
+        out = _fp4_out(out, n_rows, x2.shape[1], fmt, experts, x)
+        sharq_quantize_fp4(x2.data_ptr(), x.dtype, x2.shape[0], max(x2.stride(0), x2.shape[1]), _ptr(rows), _ptr(count),
+                           _ptr(gamma), eps, amax, out.struct)
+    return out
+
+
+def quantize_fp4_swiglu(gate: torch.Tensor, up: torch.Tensor, fmt, amax: float = 0.0,
+                        count: torch.Tensor | None = None, out: FP4Matrix | None = None, stream=None) -> FP4Matrix:
+    """SiLU(gate) * up (t, k) as an FP4 matrix; the halves of one (t, 2k) product need no copy."""
+    if gate.shape != up.shape or gate.dtype != up.dtype:
+        raise ValueError("gate and up must have one shape and dtype")
+    _same_device(gate, up=up, count=count)
+    with _place(gate, stream):
+        gate, up = _rows_of(gate, "gate"), _rows_of(up, "up")
+        if gate.stride(0) != up.stride(0):
+            gate, up = gate.contiguous(), up.contiguous()
+        if count is not None:
+            count = _i32(count, "count", (1,))
+        t, k = gate.shape
+        out = _fp4_out(out, t, k, fmt, 1, gate)
+        sharq_quantize_fp4_swiglu(gate.data_ptr(), up.data_ptr(), gate.dtype, max(gate.stride(0), k), _ptr(count), amax,
+                                  out.struct)
+    return out
+
+
+def _aligned(x: torch.Tensor) -> torch.Tensor:
+    x = x.contiguous()
+    return x if x.data_ptr() % 16 == 0 else x.clone()
+
+
+def _product_out(out, rows: int, n: int, dtype, a: FP4Matrix) -> torch.Tensor:
+    if out is None:
+        return torch.empty((rows, n), dtype=dtype, device=a.device)
+    if tuple(out.shape) != (rows, n) or not out.is_contiguous() or out.device != a.device:
+        raise ValueError(f"out must be a contiguous ({rows}, {n}) tensor on {a.device}")
+    return out
+
+
+def linear_fp4(a: FP4Matrix, w: FP4Matrix, out_dtype=torch.bfloat16, out: torch.Tensor | None = None,
+               stream=None) -> torch.Tensor:
+    """y = a w^T, (rows of a, rows of w)."""
+    _same_device(a.codes, weight=w.codes)
+    with _place(a.codes, stream):
+        out = _product_out(out, a.rows, w.rows, out_dtype, a)
+        sharq_linear_fp4(a.struct, w.struct, out.data_ptr(), out.dtype)
+    return out
+
+
+def linear_fp4_grouped(a: FP4Matrix, w: FP4Matrix, offsets: torch.Tensor, out_dtype=torch.bfloat16,
+                       out: torch.Tensor | None = None, stream=None) -> torch.Tensor:
+    """Rows [offsets[e], offsets[e + 1]) of a times expert e's weight.  Rows outside every
+    group are left as they were (undefined in an ``out`` allocated here)."""
+    _same_device(a.codes, weight=w.codes, offsets=offsets)
+    with _place(a.codes, stream):
+        offsets = _i32(offsets, "offsets", (w.experts + 1,))
+        out = _product_out(out, a.rows, w.rows, out_dtype, a)
+        sharq_linear_fp4_grouped(a.struct, w.struct, offsets.data_ptr(), out.data_ptr(), out.dtype)
+    return out
+
+
+def route(logits: torch.Tensor, top_k: int, score="softmax", bias: torch.Tensor | None = None, groups: int = 1,
+          top_groups: int = 1, group_top: int = 1, renormalize: bool = True, scale: float = 1.0,
+          stream=None) -> tuple[torch.Tensor, torch.Tensor]:
+    """Expert ids (t, top_k) int32 and weights (t, top_k) fp32 of the tokens' logits (t, experts)."""
+    if logits.dim() != 2:
+        raise ValueError(f"logits must be (t, experts), has {logits.dim()} dimensions")
+    _same_device(logits, bias=bias)
+    with _place(logits, stream):
+        t, experts = logits.shape
+        if logits.stride(1) != 1 or logits.stride(0) < experts:
+            logits = logits.contiguous()
+        if bias is not None:
+            if tuple(bias.shape) != (experts,):
+                raise ValueError(f"bias must have shape ({experts},)")
+            bias = bias.float().contiguous()
+        ids = torch.empty((t, top_k), dtype=torch.int32, device=logits.device)
+        weights = torch.empty((t, top_k), dtype=torch.float32, device=logits.device)
+        sharq_route(logits.data_ptr(), logits.dtype, t, experts, max(logits.stride(0), experts), _ptr(bias), score,
+                    groups, top_groups, group_top, top_k, renormalize, scale, ids.data_ptr(), weights.data_ptr())
+    return ids, weights
+
+
+class RoutedRows(NamedTuple):
+    """Routed-row layout of an assignment: token of each row (-1: padding), (experts + 1) offsets, row of each place."""
+
+    rows: torch.Tensor
+    offsets: torch.Tensor
+    slots: torch.Tensor
+
+
+def route_rows(ids: torch.Tensor, experts: int, stream=None) -> RoutedRows:
+    """Rows of an assignment ids (t, top_k), grouped by expert, each group padded to 128 rows.  Nothing is read
+    back: ``rows`` has the size that any assignment of this shape fits in; offsets[-1] rows of it are in use."""
+    if ids.dim() != 2:
+        raise ValueError(f"ids must be (t, top_k), has {ids.dim()} dimensions")
+    with _place(ids, stream):
+        ids = _i32(ids, "ids")
+        t, top_k = ids.shape
+        capacity = sharq_route_rows_capacity(t, top_k, experts)
+        rows = torch.empty(capacity, dtype=torch.int32, device=ids.device)
+        offsets = torch.empty(experts + 1, dtype=torch.int32, device=ids.device)
+        slots = torch.empty((t, top_k), dtype=torch.int32, device=ids.device)
+        sharq_route_rows(ids.data_ptr(), t, top_k, experts, rows.data_ptr(), capacity, offsets.data_ptr(),
+                         slots.data_ptr())
+    return RoutedRows(rows, offsets, slots)
+
+
+def combine(y: torch.Tensor, slots: torch.Tensor, weights: torch.Tensor, add: torch.Tensor | None = None,
+            out_dtype=None, out: torch.Tensor | None = None, stream=None) -> torch.Tensor:
+    """out[t] = add[t] + sum_j weights[t, j] * y[slots[t, j]] (places with a slot below 0 are left out)."""
+    if y.dim() != 2 or slots.dim() != 2:
+        raise ValueError("y must be (rows, n), slots (t, top_k)")
+    _same_device(y, slots=slots, weights=weights, add=add, out=out)
+    with _place(y, stream):
+        t, top_k = slots.shape
+        n = y.shape[1]
+        slots = _i32(slots, "slots")
+        if weights.dtype != torch.float32 or tuple(weights.shape) != (t, top_k):
+            raise ValueError(f"weights must be fp32 ({t}, {top_k})")
+        if add is not None:
+            if tuple(add.shape) != (t, n) or add.dtype != y.dtype:
+                raise ValueError(f"add must be ({t}, {n}) of y's dtype")
+            add = _aligned(add)
+        if out is None:
+            out = torch.empty((t, n), dtype=out_dtype or y.dtype, device=y.device)
+        elif tuple(out.shape) != (t, n) or not out.is_contiguous():
+            raise ValueError(f"out must be a contiguous ({t}, {n}) tensor")
+        y, weights = _aligned(y), weights.contiguous()
+        sharq_combine(y.data_ptr(), y.dtype, y.shape[0], n, slots.data_ptr(), weights.data_ptr(), t, top_k, _ptr(add),
+                      out.data_ptr(), out.dtype)
     return out

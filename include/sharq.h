@@ -288,6 +288,137 @@ sharq_status sharq_linear_grouped_gather(const sharq_prepared* tokens, const int
                                          const sharq_weight* w, const int32_t* group_offsets, void* y,
                                          sharq_dtype y_dt, sharq_stream stream);
 
+/* ---------------------------------------------------------------------------
+ * Plain microscaled FP4 layers and mixture-of-experts routing.
+ *
+ * The layers above split every activation row into two FP4 operands.  The calls
+ * below are the plain form (one FP4 operand a row, a third of the MMA work) and
+ * the routing around a mixture-of-experts layer, so that a layer runs without
+ * the host:
+ *   sharq_route         logits -> expert ids and weights of every token;
+ *   sharq_route_rows    ids -> routed rows, grouped by expert (the `rows` and
+ *                       `group_offsets` of every grouped call here);
+ *   sharq_quantize_fp4  rows (gathered by `rows`) -> FP4;
+ *   sharq_linear_fp4_grouped, sharq_quantize_fp4_swiglu, ... the experts;
+ *   sharq_combine       the experts' rows -> tokens.
+ * They are inference operators, like the rest of the library. */
+
+/* A microscaled FP4 matrix of `experts` stacked blocks of `rows` rows: weights
+ * (rows = outputs) and activations (experts = 1) alike.
+ *   codes      experts * rows * k/2 bytes, row-major;
+ *   scales     per expert, tiled scale layout, `rows` rows, k/b scales a row (b =
+ *              16 NVFP4, 32 MXFP4); the places of a row past its k/b scales are 0,
+ *              those of rows past the last one are not written;
+ *   row_scale  experts * rows floats: the second-level scale, one for each ROW
+ *              (NVFP4: A/2688 with A the row's largest magnitude, MXFP4: 1).  A
+ *              row's FP4 form then depends on that row alone, not on the batch
+ *              it is quantized in, and one pass over the input is enough.
+ * Value of element (r, j): E2M1(code) * scale(r, j / b) * row_scale(r).
+ * Shapes: rows >= 1; k a positive multiple of 32. */
+typedef struct {
+  void* codes;
+  void* scales;
+  float* row_scale;
+  int64_t rows, k;
+  int32_t experts;
+  sharq_format fmt;
+} sharq_fp4;
+
+/* Byte sizes of the buffers of a sharq_fp4 (all experts together). */
+sharq_status sharq_fp4_sizes(int64_t rows, int64_t k, int32_t experts, sharq_format fmt, size_t* codes_bytes,
+                             size_t* scales_bytes, size_t* row_scale_bytes);
+
+/* Quantizes rows of x to FP4:
+ *   h = RMSNorm(x) * gamma if gamma != NULL (fp32, as in sharq_prepare), else x;
+ *   MXFP4: per 32 elements e = floor(log2 amax) - 2, element = E2M1(h / 2^e);
+ *   NVFP4: A = max |h| of the row (or `amax` if > 0), g = 2688 / A, per 16 elements
+ *          S = E4M3((amax / 6) * g), element = E2M1(h * (g / S)) (0 if S = 0);
+ * each step rounded once in fp32, E2M1 and E4M3 to nearest even, saturating.
+ * x: x_rows rows of k values of dtype x_dt, row r at x + r * x_stride (elements;
+ * >= k, rows 16-byte aligned).  rows == NULL: x_rows must be out->rows *
+ * out->experts.  rows != NULL (out->experts 1): DEVICE, out->rows int32 values;
+ * row i is quantized from x row rows[i], or from a zero row if rows[i] is not in
+ * [0, x_rows).  count: NULL, or a DEVICE int32: rows from *count on (out->experts
+ * 1) are left as they were (sharq_route_rows leaves the rows in use in
+ * group_offsets[experts]).  A row with NaN or infinities has no defined value;
+ * the other rows keep theirs. */
+sharq_status sharq_quantize_fp4(const void* x, sharq_dtype x_dt, int64_t x_rows, int64_t x_stride,
+                                const int32_t* rows, const int32_t* count, const void* gamma, float eps, float amax,
+                                sharq_fp4* out, sharq_stream stream);
+
+/* The same from a gated MLP's two inputs: h = SiLU(gate) * up (as in
+ * sharq_prepare_swiglu), both with row stride `stride` (the two halves of one
+ * gate/up product need no copy). */
+sharq_status sharq_quantize_fp4_swiglu(const void* gate, const void* up, sharq_dtype dt, int64_t stride,
+                                       const int32_t* count, float amax, sharq_fp4* out, sharq_stream stream);
+
+/* y[t][n] = sum_j X[t][j] * W[n][j] over the values of two FP4 matrices of one
+ * format and k (fp32 accumulation, rounded once to y_dt; as in every fp32 sum, a
+ * value whose terms' magnitudes add up to 2^128 or more may be non-finite).  x->experts and
+ * w->experts 1; w->rows (n) a multiple of 8.  y: x->rows * n row-major, 16-byte
+ * aligned.  Results repeat bit for bit. */
+sharq_status sharq_linear_fp4(const sharq_fp4* x, const sharq_fp4* w, void* y, sharq_dtype y_dt, sharq_stream stream);
+
+/* The grouped form: rows [off[e], off[e+1]) of x are multiplied by expert e's
+ * weight.  group_offsets: DEVICE, w->experts + 1 int32, non-decreasing multiples of
+ * 128, the last <= x->rows rounded up to 128.  Rows of y outside every group are
+ * left as they were. */
+sharq_status sharq_linear_fp4_grouped(const sharq_fp4* x, const sharq_fp4* w, const int32_t* group_offsets, void* y,
+                                      sharq_dtype y_dt, sharq_stream stream);
+
+typedef enum { SHARQ_SOFTMAX = 0, SHARQ_SIGMOID = 1 } sharq_score;
+
+#define SHARQ_MAX_EXPERTS 512 /* sharq_route, sharq_route_rows */
+#define SHARQ_MAX_TOP_K 32
+
+/* Routing of t tokens to top_k of `experts` experts each:
+ *   p = softmax(l) or sigmoid(l) over the token's logits l;  c = p + bias (bias NULL: p);
+ *   an expert is eligible if l and c are neither NaN nor -inf (a mask of -inf
+ *   takes an expert out; it counts for no softmax sum either);
+ *   groups > 1: experts / groups adjacent experts form a group, whose value is the
+ *   sum of its group_top (1 or 2) largest eligible c; the top_groups groups of
+ *   largest value stay (ties to the lower group);
+ *   ids = the top_k eligible experts of those by c, largest first, ties to the lower
+ *   index (without a bias by l itself, which p rises with);
+ *   weights = p of the ids (without the bias), divided by their sum if renormalize,
+ *   times scale.
+ * A token with fewer eligible experts has id -1 and weight 0 in the places left.
+ * Selection is as in 64 bits (values that differ are told apart whatever fp32 rounds
+ * them to); weights are fp32.
+ * logits: t rows of `experts` values of dtype dt, row r at logits + r * stride
+ * elements.  bias: experts floats or NULL.  ids, weights: t * top_k.
+ * experts <= SHARQ_MAX_EXPERTS, a multiple of groups; groups <= 32; top_k <=
+ * SHARQ_MAX_TOP_K and <= top_groups * (experts / groups). */
+sharq_status sharq_route(const void* logits, sharq_dtype dt, int64_t t, int32_t experts, int64_t stride,
+                         const float* bias, sharq_score score, int32_t groups, int32_t top_groups, int32_t group_top,
+                         int32_t top_k, int32_t renormalize, float scale, int32_t* ids, float* weights,
+                         sharq_stream stream);
+
+/* Rows that hold any assignment of t tokens to top_k experts each, every expert's
+ * rows padded to a multiple of 128 (a multiple of 128). */
+sharq_status sharq_route_rows_capacity(int64_t t, int32_t top_k, int32_t experts, int64_t* capacity);
+
+/* Routed-row layout of an assignment (in token order inside each expert, so that
+ * it repeats):
+ *   group_offsets  experts + 1: expert e's rows are [off[e], off[e+1]), multiples of 128;
+ *   rows           capacity: the token of each routed row, -1 for padding rows and
+ *                  for every row from off[experts] on;
+ *   slots          t * top_k: the routed row of each (token, place), -1 for an id
+ *                  outside [0, experts) (which gets no row).
+ * ids: t * top_k.  The same expert twice in a token gets two rows.  capacity: at
+ * least sharq_route_rows_capacity's (SHARQ_ERR_WORKSPACE if less).  All DEVICE. */
+sharq_status sharq_route_rows(const int32_t* ids, int64_t t, int32_t top_k, int32_t experts, int32_t* rows,
+                              int64_t capacity, int32_t* group_offsets, int32_t* slots, sharq_stream stream);
+
+/* The experts' rows back to their tokens:
+ *   out[t] = add[t] + sum_j weights[t][j] * y[slots[t][j]]   (add NULL: 0)
+ * in fp32, added in the order of j, rounded once to out_dt.  Places whose slot is
+ * outside [0, y_rows) are left out.  y: y_rows * n, add: t * n, both of dtype y_dt;
+ * out: t * n (may be add); n a multiple of 8; all 16-byte aligned. */
+sharq_status sharq_combine(const void* y, sharq_dtype y_dt, int64_t y_rows, int64_t n, const int32_t* slots,
+                           const float* weights, int64_t t, int32_t top_k, const void* add, void* out,
+                           sharq_dtype out_dt, sharq_stream stream);
+
 /* Synchronizes the stream, then reports and clears this device's error word. */
 sharq_status sharq_sync_status(sharq_stream stream);
 
