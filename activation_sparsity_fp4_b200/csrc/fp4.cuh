@@ -6,6 +6,8 @@
 
 namespace sharq {
 
+constexpr int64_t kFp4MaxHeld = 16384;  // longest row that fp4_kernel holds in registers (32 warps x 32 units)
+
 enum { FRONT_NONE = 0, FRONT_NORM = 1, FRONT_SWIGLU = 2 };
 
 struct Fp4Params {
@@ -45,6 +47,233 @@ __device__ __forceinline__ void fp4_load16(const Fp4Params& p, int64_t at, float
   }
 }
 
+// ------------------------------------------------- a row in registers
+// wpr warps share a row, a lane holds NJ units of 16 adjacent values (unit
+// w * 32 + lane + 32 wpr j of the row), read once.  The row's sum of squares and
+// largest magnitude are reduced by shuffles and, across its warps, through
+// shared memory behind a barrier of those warps alone.
+// WIDE: up to 32 warps a row, else up to 8.
+template <bool MAX, bool WIDE>
+__device__ __forceinline__ float row_reduce(float v, float* red /* wpr floats, a multiple of 8 */, int wr, int wpr,
+                                            int barrier) {
+#pragma unroll
+  for (int m = 16; m >= 1; m >>= 1) {
+    const float o = __shfl_xor_sync(0xffffffffu, v, m);
+    v = MAX ? fmaxf(v, o) : __fadd_rn(v, o);
+  }
+  if (wpr > 1) {
+    const int lane = threadIdx.x & 31, slots = WIDE ? (wpr + 7) & ~7 : 8;
+    if (lane == 0) red[wr] = v;
+    if (wr == 0 && lane >= wpr && lane < slots) red[lane] = 0.0f;  // adds nothing, and no magnitude is smaller
+    asm volatile("bar.sync %0, %1;" ::"r"(barrier), "r"(wpr * 32) : "memory");
+    for (int i = 0; i < (WIDE ? slots : 8); i += 8) {
+      const float4 c = *reinterpret_cast<const float4*>(red + i), d = *reinterpret_cast<const float4*>(red + i + 4);
+      const float t = MAX ? fmaxf(fmaxf(fmaxf(c.x, c.y), fmaxf(c.z, c.w)), fmaxf(fmaxf(d.x, d.y), fmaxf(d.z, d.w)))
+                          : __fadd_rn(__fadd_rn(__fadd_rn(c.x, c.y), __fadd_rn(c.z, c.w)),
+                                      __fadd_rn(__fadd_rn(d.x, d.y), __fadd_rn(d.z, d.w)));
+      v = i == 0 ? t : (MAX ? fmaxf(v, t) : __fadd_rn(v, t));
+    }
+  }
+  return v;
+}
+
+// Scale code of a block with the largest magnitude a, and the factor onto the E2M1 grid.
+template <int FMT>
+__device__ __forceinline__ uint32_t fp4_scale(float a, float g_enc, float& mul) {
+  if constexpr (FMT == FMT_MX) {
+    const int ex = mx_exponent(a);
+    mul = pow2f(-ex);
+    return (uint32_t)(ex + 127);
+  } else {
+    const uint32_t sc = cvt_e4m3(__fmul_rn(div6_rn(a), g_enc));
+    mul = sc == 0 ? 0.0f : __fdiv_rn(g_enc, e4m3_value(sc));
+    return sc;
+  }
+}
+
+// The 16 values of a unit as they are in memory.
+template <int FRONT, bool XBF16>
+struct Fp4Raw {
+  static constexpr int kWords = (XBF16 ? 2 : 4) * (FRONT == FRONT_SWIGLU ? 2 : 1);
+  uint4 q[kWords];
+  __device__ __forceinline__ void load(const Fp4Params& p, int64_t at) {
+    const uint4* x = reinterpret_cast<const uint4*>(static_cast<const uint8_t*>(p.x) + at * (XBF16 ? 2 : 4));
+#pragma unroll
+    for (int i = 0; i < (XBF16 ? 2 : 4); i++) q[i] = __ldg(x + i);
+    if constexpr (FRONT == FRONT_SWIGLU) {
+      const uint4* y = reinterpret_cast<const uint4*>(static_cast<const uint8_t*>(p.x2) + at * (XBF16 ? 2 : 4));
+#pragma unroll
+      for (int i = 0; i < (XBF16 ? 2 : 4); i++) q[kWords / 2 + i] = __ldg(y + i);
+    }
+  }
+  __device__ __forceinline__ void zero() {
+#pragma unroll
+    for (int i = 0; i < kWords; i++) q[i] = make_uint4(0u, 0u, 0u, 0u);
+  }
+  __device__ __forceinline__ static void unpack(const uint4* w, float (&v)[16]) {
+#pragma unroll
+    for (int i = 0; i < (XBF16 ? 2 : 4); i++) {
+      const uint32_t ws[4] = {w[i].x, w[i].y, w[i].z, w[i].w};
+#pragma unroll
+      for (int j = 0; j < 4; j++) {
+        if constexpr (XBF16) {
+          v[8 * i + 2 * j] = __uint_as_float(ws[j] << 16);
+          v[8 * i + 2 * j + 1] = __uint_as_float(ws[j] & 0xFFFF0000u);
+        } else {
+          v[4 * i + j] = __uint_as_float(ws[j]);
+        }
+      }
+    }
+  }
+  __device__ __forceinline__ void values(float (&v)[16]) const {
+    unpack(q, v);
+    if constexpr (FRONT == FRONT_SWIGLU) {
+      uint32_t any = 0;  // padding rows hold zeros: SiLU(0) * 0 = 0 without the exponentials
+#pragma unroll
+      for (int i = 0; i < kWords; i++) any |= q[i].x | q[i].y | q[i].z | q[i].w;
+      if (any == 0) return;
+      float u[16];
+      unpack(q + kWords / 2, u);
+#pragma unroll
+      for (int i = 0; i < 16; i++) v[i] = __fmul_rn(dev_silu(v[i]), u[i]);
+    }
+  }
+};
+
+// Persistent over rows; the next row's loads are issued before the present
+// row's arithmetic, so that both the memory and the issue slots stay busy.
+template <int FMT, int FRONT, bool XBF16, int NJ>
+__global__ void __launch_bounds__(NJ == 1 ? 1024 : 256) fp4_kernel(const Fp4Params p, const int wpr) {
+  // [row parity][sum, sum again, largest magnitude][eight for each row of the block, or 32 for its only one]
+  __shared__ __align__(16) float red[2][3][64];
+  grid_dep_wait();
+  grid_dep_launch();
+  const int lane = threadIdx.x & 31, w = threadIdx.x >> 5, group = w / wpr, wr = w - group * wpr;
+  const int groups = (int)(blockDim.x / (32 * wpr)), bar = 1 + group;
+  const int units = (int)(p.k / 16), u0 = wr * 32 + lane, step = 32 * wpr;
+  int64_t end = p.rows_out;
+  if (p.count) {
+    const int64_t c = (int64_t)__ldg(p.count);
+    end = c < end ? c : end;
+  }
+  const int64_t stride = (int64_t)gridDim.x * groups;
+  int64_t r = (int64_t)blockIdx.x * groups + group;
+  auto source = [&](int64_t row) -> int64_t {
+    if (row >= end) return -1;
+    const int64_t src = p.rows ? (int64_t)__ldg(p.rows + row) : row;
+    return src < p.x_rows ? src : -1;
+  };
+  Fp4Raw<FRONT, XBF16> raw[NJ];
+  auto fetch = [&](int64_t src) {
+#pragma unroll
+    for (int j = 0; j < NJ; j++) {
+      const int u = u0 + step * j;
+      if (src >= 0 && u < units) raw[j].load(p, src * p.stride + 16 * u);
+      else raw[j].zero();
+    }
+  };
+  fetch(source(r));
+  int64_t next = source(r + stride);
+  constexpr int kStep = FMT == FMT_NV ? 1 : 2;  // lanes per scale
+  const int64_t S = p.k / (16 * kStep);
+  for (int par = 0; r < end; r += stride, par ^= 1) {
+    float v[NJ][16];
+#pragma unroll
+    for (int j = 0; j < NJ; j++) raw[j].values(v[j]);
+    fetch(next);
+    next = source(r + 2 * stride);
+    if constexpr (FRONT == FRONT_NORM) {
+      float lo = 0.0f, hi = 0.0f;
+#pragma unroll
+      for (int j = 0; j < NJ; j++)
+#pragma unroll
+        for (int i = 0; i < 16; i += 2) {
+          float x = v[j][i], y = v[j][i + 1];
+          fma2(x, y, x, y, lo, hi);
+          lo = x;
+          hi = y;
+        }
+      const float s = row_reduce<false, NJ == 1>(__fadd_rn(lo, hi), red[par][0] + 8 * group, wr, wpr, bar);
+      float rs;
+      if (isinf(s)) {  // squares beyond fp32 (from about 2^64 / sqrt(k) on): again at 2^-80 of their size, eps is nothing
+        float t = 0.0f;
+#pragma unroll
+        for (int j = 0; j < NJ; j++)
+#pragma unroll
+          for (int i = 0; i < 16; i++) t = __fmaf_rn(v[j][i] * 0x1p-80f, v[j][i] * 0x1p-80f, t);
+        rs = 0x1p-80f * rstd_from_sumsq(row_reduce<false, NJ == 1>(t, red[par][1] + 8 * group, wr, wpr, bar), p.k, 0.0f);
+      } else {
+        rs = rstd_from_sumsq(s, p.k, p.eps);
+      }
+#pragma unroll
+      for (int j = 0; j < NJ; j++) {
+        const int u = u0 + step * j;
+        if (u >= units) continue;
+#pragma unroll
+        for (int h = 0; h < 2; h++) {
+          float g[8];
+          load8<XBF16>(p.gamma, 16 * u + 8 * h, g);
+#pragma unroll
+          for (int i = 0; i < 8; i += 2) {
+            mul2(v[j][8 * h + i], v[j][8 * h + i + 1], rs, rs);
+            mul2(v[j][8 * h + i], v[j][8 * h + i + 1], g[i], g[i + 1]);
+          }
+        }
+      }
+    }
+    float a[NJ], top = 0.0f;
+#pragma unroll
+    for (int j = 0; j < NJ; j++) {
+      a[j] = 0.0f;
+#pragma unroll
+      for (int i = 0; i < 16; i++) a[j] = fmaxf(a[j], fabsf(v[j][i]));
+      top = fmaxf(top, a[j]);
+    }
+    float g_enc = 1.0f;
+    if constexpr (FMT == FMT_NV) {
+      float g_dec;
+      top = p.amax > 0.0f ? p.amax : row_reduce<true, NJ == 1>(top, red[par][2] + 8 * group, wr, wpr, bar);
+      tensor_scales(top, g_enc, g_dec);
+      if (u0 == 0) p.row_scale[r] = g_dec;
+    } else if (u0 == 0) {
+      p.row_scale[r] = 1.0f;
+    }
+    int64_t e = 0, re = r;
+    if (p.rows_expert != p.rows_out) {
+      e = r / p.rows_expert;
+      re = r % p.rows_expert;
+    }
+    uint8_t* sf = p.scales + e * tiled_sf_bytes(p.rows_expert, S) + tiled_sf_offset(re, u0 / kStep, S);
+    uint8_t* codes = p.codes + r * (p.k / 2) + 8 * u0;
+#pragma unroll
+    for (int j = 0; j < NJ; j++) {
+      const bool in = u0 + step * j < units;
+      float am = a[j], mul;
+      if constexpr (FMT == FMT_MX) am = fmaxf(am, __shfl_xor_sync(0xffffffffu, am, 1));
+      uint32_t sc = fp4_scale<FMT>(am, g_enc, mul);
+      if (in) {
+        uint32_t q[2];
+#pragma unroll
+        for (int h = 0; h < 2; h++) {
+          float* vv = v[j] + 8 * h;
+#pragma unroll
+          for (int i = 0; i < 8; i += 2) mul2(vv[i], vv[i + 1], mul, mul);
+          q[h] = mul == 0.0f ? 0u : cvt_e2m1x8(vv);
+        }
+        *reinterpret_cast<uint2*>(codes + (int64_t)8 * step * j) = make_uint2(q[0], q[1]);
+      } else {
+        sc = 0;  // the places of a group of four past the row's last scale
+      }
+      // four adjacent scales of a row are one word of the tiled layout (512 bytes on: the next four)
+      sc |= __shfl_down_sync(0xffffffffu, sc, kStep) << 8;
+      sc |= __shfl_down_sync(0xffffffffu, sc, 2 * kStep) << 16;
+      if (lane % (4 * kStep) == 0 && in)
+        *reinterpret_cast<uint32_t*>(sf + (int64_t)(step / (4 * kStep)) * 512 * j) = sc;
+    }
+  }
+}
+
+// ------------------------------------- rows too long for the registers
 template <bool MAX>
 __device__ __forceinline__ float block_reduce(float v, float* red) {  // 128 threads
 #pragma unroll
@@ -59,9 +288,10 @@ __device__ __forceinline__ float block_reduce(float v, float* red) {  // 128 thr
              : __fadd_rn(__fadd_rn(red[0], red[1]), __fadd_rn(red[2], red[3]));
 }
 
-// One block of 128 threads per row; a thread takes 16 values at a time.
+// One block of 128 threads per row; a thread takes 16 values at a time and reads
+// them again (from L1 or L2) for each pass over the row.
 template <int FMT, int FRONT, bool XBF16>
-__global__ void __launch_bounds__(128) fp4_kernel(const Fp4Params p) {
+__global__ void __launch_bounds__(128) fp4_long_kernel(const Fp4Params p) {
   __shared__ float red[4];
   grid_dep_wait();
   grid_dep_launch();
@@ -129,18 +359,9 @@ __global__ void __launch_bounds__(128) fp4_kernel(const Fp4Params p) {
     float a = 0.0f;
 #pragma unroll
     for (int i = 0; i < 16; i++) a = fmaxf(a, fabsf(v[i]));
-    uint32_t sc;
+    if constexpr (FMT == FMT_MX) a = fmaxf(a, __shfl_xor_sync(0xffffffffu, a, 1));
     float mul;
-    if constexpr (FMT == FMT_MX) {
-      a = fmaxf(a, __shfl_xor_sync(0xffffffffu, a, 1));
-      const int ex = mx_exponent(a);
-      sc = (uint32_t)(ex + 127);
-      mul = pow2f(-ex);
-    } else {
-      sc = cvt_e4m3(__fmul_rn(div6_rn(a), g_enc));
-      const float sv = e4m3_value(sc);
-      mul = sv == 0.0f ? 0.0f : __fdiv_rn(g_enc, sv);
-    }
+    const uint32_t sc = fp4_scale<FMT>(a, g_enc, mul);
     if (u < units) {
       const uint2 q = make_uint2(quant8(v, mul), quant8(v + 8, mul));
       *reinterpret_cast<uint2*>(p.codes + r * (p.k / 2) + 8 * (int64_t)u) = q;

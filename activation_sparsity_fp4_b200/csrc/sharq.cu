@@ -772,9 +772,33 @@ sharq_status check_rows(const void* x, sharq_dtype dt, int64_t stride, int64_t k
   return SHARQ_OK;
 }
 
+template <int FMT, int FRONT, bool XBF16, int NJ>
+sharq_status launch_fp4_rows(const Fp4Params& fp, cudaStream_t s) {
+  const int wpr = (int)((fp.k / 16 + 32 * NJ - 1) / (32 * NJ)), rows = wpr > 8 ? 1 : 8 / wpr, threads = 32 * wpr * rows;
+  static std::atomic<int> cached[33];  // resident blocks an SM, by warps per row
+  int per_sm = cached[wpr].load(std::memory_order_relaxed);
+  if (per_sm == 0) {
+    if (cudaOccupancyMaxActiveBlocksPerMultiprocessor(&per_sm, fp4_kernel<FMT, FRONT, XBF16, NJ>, threads, 0) != cudaSuccess ||
+        per_sm < 1) {
+      (void)cudaGetLastError();
+      per_sm = 1;
+    }
+    cached[wpr].store(per_sm, std::memory_order_relaxed);
+  }
+  const int64_t want = (fp.rows_out + rows - 1) / rows, cap = (int64_t)sm_count() * per_sm;
+  return launch_ex(fp4_kernel<FMT, FRONT, XBF16, NJ>, dim3((unsigned)(want < cap ? want : cap)), dim3(threads), 0, s, 1,
+                   fp, wpr);
+}
 template <int FMT, int FRONT, bool XBF16>
 sharq_status launch_fp4(const Fp4Params& fp, cudaStream_t s) {
-  return launch_ex(fp4_kernel<FMT, FRONT, XBF16>, dim3((unsigned)fp.rows_out), dim3(128), 0, s, 1, fp);
+  if (fp.k > kFp4MaxHeld)
+    return launch_ex(fp4_long_kernel<FMT, FRONT, XBF16>, dim3((unsigned)fp.rows_out), dim3(128), 0, s, 1, fp);
+  // Units of 16 a lane: one where every row has an SM to itself and the most lanes finish it soonest (1 x 14336 with
+  // SwiGLU: 4.7 us against 8.3 with four), else two (32768 x 5120 behind a norm: 118 us against 161 with four, whose
+  // registers leave too few warps), four only for rows that eight warps cannot hold otherwise.
+  if (fp.k <= 512 || fp.rows_out <= sm_count()) return launch_fp4_rows<FMT, FRONT, XBF16, 1>(fp, s);
+  if (fp.k <= 8192) return launch_fp4_rows<FMT, FRONT, XBF16, 2>(fp, s);
+  return launch_fp4_rows<FMT, FRONT, XBF16, 4>(fp, s);
 }
 template <int FRONT>
 sharq_status fp4_dispatch(const Fp4Params& fp, sharq_format fmt, bool bf16, cudaStream_t s) {

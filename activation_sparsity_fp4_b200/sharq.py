@@ -10,6 +10,7 @@ from __future__ import annotations
 
 import contextlib
 import ctypes
+import functools
 import os
 from typing import NamedTuple
 
@@ -20,6 +21,7 @@ from . import build_ext
 MXFP4, NVFP4 = 0, 1
 NM_2_4, NM_4_8_PAIR, NM_8_16, NM_8_16_PAIR = 0, 1, 2, 3
 F32, BF16 = 0, 1
+DTYPES = {torch.float32: F32, torch.bfloat16: BF16}
 FORMATS = {"mxfp4": MXFP4, "nvfp4": NVFP4}
 SCORES = {"softmax": 0, "sigmoid": 1}
 PATTERNS = {"2:4": NM_2_4, "4:8pair": NM_4_8_PAIR, "8:16": NM_8_16, "8:16pair": NM_8_16_PAIR}
@@ -123,7 +125,8 @@ def _check(status: int, where: str):
 
 def _stream(stream=None):
     if stream is None:
-        stream = torch.cuda.current_stream()
+        # the handle of torch.cuda.current_stream() without the Stream object around it (0.1 instead of 3 us a call)
+        return torch._C._cuda_getCurrentRawStream(torch.cuda.current_device())
     return ctypes.c_void_p(stream.cuda_stream if hasattr(stream, "cuda_stream") else int(stream))
 
 
@@ -141,11 +144,9 @@ def _pat(p) -> int:
 
 def _dt(d) -> int:
     if isinstance(d, torch.dtype):
-        if d == torch.bfloat16:
-            return BF16
-        if d == torch.float32:
-            return F32
-        raise ValueError(f"unsupported dtype {d}")
+        if d not in DTYPES:
+            raise ValueError(f"unsupported dtype {d}")
+        return DTYPES[d]
     return int(d)
 
 
@@ -266,6 +267,7 @@ def sharq_route(logits_ptr: int, dt, t: int, experts: int, stride: int, bias_ptr
            "sharq_route")
 
 
+@functools.lru_cache(maxsize=1024)
 def sharq_route_rows_capacity(t: int, top_k: int, experts: int) -> int:
     out = ctypes.c_int64(0)
     _check(lib().sharq_route_rows_capacity(t, top_k, experts, ctypes.byref(out)), "sharq_route_rows_capacity")
@@ -439,23 +441,26 @@ def _on(x: torch.Tensor, stream):
     """Allocate and launch where x lives: its device, and the given stream (default: that device's current one)."""
     if not x.is_cuda:
         raise ValueError("a CUDA tensor is needed")
+    if isinstance(stream, int):
+        stream = torch.cuda.ExternalStream(stream, device=x.device)
     with torch.cuda.device(x.device), torch.cuda.stream(stream):
         yield
 
 
+_HERE = contextlib.nullcontext()
+
+
 def _place(x: torch.Tensor, stream):
     # the usual call, on the current device's current stream, needs no context at all
-    if stream is None and x.is_cuda and x.device.index == torch.cuda.current_device():
-        return contextlib.nullcontext()
-    if isinstance(stream, int):
-        stream = torch.cuda.ExternalStream(stream, device=x.device)
+    if stream is None and x.is_cuda and x.get_device() == torch.cuda.current_device():
+        return _HERE
     return _on(x, stream)
 
 
-def _same_device(x: torch.Tensor, **others):
-    for name, o in others.items():
-        if o is not None and o.device != x.device:
-            raise ValueError(f"{name} is on {o.device}, the call's first tensor on {x.device}")
+def _same_device(x: torch.Tensor, *others):
+    for o in others:
+        if o is not None and o.get_device() != x.get_device():
+            raise ValueError(f"tensors on {x.device} and {o.device} in one call")
 
 
 def _rows_of(x: torch.Tensor, what: str) -> torch.Tensor:
@@ -480,21 +485,40 @@ def _ptr(x: torch.Tensor | None):
     return None if x is None else x.data_ptr()
 
 
+@functools.lru_cache(maxsize=1024)
+def _fp4_layout(rows: int, k: int, experts: int, fmt: int) -> tuple[int, int, int]:
+    """Offsets of the scales and row scales, and the size, of one buffer for an FP4 matrix (256-byte aligned parts)."""
+    c, s, r = sharq_fp4_sizes(rows, k, experts, fmt)
+    at = (c + 255) // 256 * 256
+    end = at + (s + 255) // 256 * 256
+    return at, end, end + r
+
+
 class FP4Matrix:
-    """Device buffers of a microscaled FP4 matrix: activations, or a weight of one or ``experts`` stacked blocks."""
+    """Device buffer of a microscaled FP4 matrix: activations, or a weight of one or ``experts`` stacked blocks."""
 
     def __init__(self, rows: int, k: int, fmt, experts: int = 1, device="cuda"):
         self.rows, self.k, self.fmt, self.experts = rows, k, _fmt(fmt), experts
-        c, s, r = sharq_fp4_sizes(rows, k, experts, self.fmt)
-        self.codes = _alloc(c, device)
-        self.scales = _alloc(s, device)
-        self.row_scale = torch.empty(experts * rows, dtype=torch.float32, device=device)
-        self.struct = sharq_fp4(self.codes.data_ptr(), self.scales.data_ptr(), self.row_scale.data_ptr(), rows, k,
-                                experts, self.fmt)
+        self._at, self._end, size = _fp4_layout(rows, k, experts, self.fmt)
+        self.buffer = torch.empty_strided((size,), (1,), dtype=torch.uint8, device=device)
+        p = self.buffer.data_ptr()
+        self.struct = sharq_fp4(p, p + self._at, p + self._end, rows, k, experts, self.fmt)
 
     @property
     def device(self):
-        return self.codes.device
+        return self.buffer.device
+
+    @property
+    def codes(self) -> torch.Tensor:
+        return self.buffer[: self.experts * self.rows * self.k // 2]
+
+    @property
+    def scales(self) -> torch.Tensor:
+        return self.buffer[self._at : self._at + sharq_fp4_sizes(self.rows, self.k, self.experts, self.fmt)[1]]
+
+    @property
+    def row_scale(self) -> torch.Tensor:
+        return self.buffer[self._end :].view(torch.float32)
 
 
 def _fp4_out(out: FP4Matrix | None, rows: int, k: int, fmt, experts: int, x: torch.Tensor) -> FP4Matrix:
@@ -513,7 +537,7 @@ def quantize_fp4(x: torch.Tensor, fmt, rows: torch.Tensor | None = None, gamma: 
     in front.  count: one int32 on the GPU; rows from it on are left as they were."""
     if x.dim() not in (2, 3):
         raise ValueError(f"x must be (t, k) or (experts, n, k), has {x.dim()} dimensions")
-    _same_device(x, rows=rows, gamma=gamma, count=count)
+    _same_device(x, rows, gamma, count)
     with _place(x, stream):
         experts = x.shape[0] if x.dim() == 3 else 1
         x2 = _rows_of(x if x.dim() == 2 else x.flatten(0, 1), "x")
@@ -537,7 +561,7 @@ def quantize_fp4_swiglu(gate: torch.Tensor, up: torch.Tensor, fmt, amax: float =
     """SiLU(gate) * up (t, k) as an FP4 matrix; the halves of one (t, 2k) product need no copy."""
     if gate.shape != up.shape or gate.dtype != up.dtype:
         raise ValueError("gate and up must have one shape and dtype")
-    _same_device(gate, up=up, count=count)
+    _same_device(gate, up, count)
     with _place(gate, stream):
         gate, up = _rows_of(gate, "gate"), _rows_of(up, "up")
         if gate.stride(0) != up.stride(0):
@@ -558,7 +582,7 @@ def _aligned(x: torch.Tensor) -> torch.Tensor:
 
 def _product_out(out, rows: int, n: int, dtype, a: FP4Matrix) -> torch.Tensor:
     if out is None:
-        return torch.empty((rows, n), dtype=dtype, device=a.device)
+        return a.buffer.new_empty((rows, n), dtype=dtype)
     if tuple(out.shape) != (rows, n) or not out.is_contiguous() or out.device != a.device:
         raise ValueError(f"out must be a contiguous ({rows}, {n}) tensor on {a.device}")
     return out
@@ -567,8 +591,8 @@ def _product_out(out, rows: int, n: int, dtype, a: FP4Matrix) -> torch.Tensor:
 def linear_fp4(a: FP4Matrix, w: FP4Matrix, out_dtype=torch.bfloat16, out: torch.Tensor | None = None,
                stream=None) -> torch.Tensor:
     """y = a w^T, (rows of a, rows of w)."""
-    _same_device(a.codes, weight=w.codes)
-    with _place(a.codes, stream):
+    _same_device(a.buffer, w.buffer)
+    with _place(a.buffer, stream):
         out = _product_out(out, a.rows, w.rows, out_dtype, a)
         sharq_linear_fp4(a.struct, w.struct, out.data_ptr(), out.dtype)
     return out
@@ -578,8 +602,8 @@ def linear_fp4_grouped(a: FP4Matrix, w: FP4Matrix, offsets: torch.Tensor, out_dt
                        out: torch.Tensor | None = None, stream=None) -> torch.Tensor:
     """Rows [offsets[e], offsets[e + 1]) of a times expert e's weight.  Rows outside every
     group are left as they were (undefined in an ``out`` allocated here)."""
-    _same_device(a.codes, weight=w.codes, offsets=offsets)
-    with _place(a.codes, stream):
+    _same_device(a.buffer, w.buffer, offsets)
+    with _place(a.buffer, stream):
         offsets = _i32(offsets, "offsets", (w.experts + 1,))
         out = _product_out(out, a.rows, w.rows, out_dtype, a)
         sharq_linear_fp4_grouped(a.struct, w.struct, offsets.data_ptr(), out.data_ptr(), out.dtype)
@@ -592,7 +616,7 @@ def route(logits: torch.Tensor, top_k: int, score="softmax", bias: torch.Tensor 
     """Expert ids (t, top_k) int32 and weights (t, top_k) fp32 of the tokens' logits (t, experts)."""
     if logits.dim() != 2:
         raise ValueError(f"logits must be (t, experts), has {logits.dim()} dimensions")
-    _same_device(logits, bias=bias)
+    _same_device(logits, bias)
     with _place(logits, stream):
         t, experts = logits.shape
         if logits.stride(1) != 1 or logits.stride(0) < experts:
@@ -601,8 +625,8 @@ def route(logits: torch.Tensor, top_k: int, score="softmax", bias: torch.Tensor 
             if tuple(bias.shape) != (experts,):
                 raise ValueError(f"bias must have shape ({experts},)")
             bias = bias.float().contiguous()
-        ids = torch.empty((t, top_k), dtype=torch.int32, device=logits.device)
-        weights = torch.empty((t, top_k), dtype=torch.float32, device=logits.device)
+        ids = logits.new_empty((t, top_k), dtype=torch.int32)
+        weights = logits.new_empty((t, top_k), dtype=torch.float32)
         sharq_route(logits.data_ptr(), logits.dtype, t, experts, max(logits.stride(0), experts), _ptr(bias), score,
                     groups, top_groups, group_top, top_k, renormalize, scale, ids.data_ptr(), weights.data_ptr())
     return ids, weights
@@ -625,9 +649,8 @@ def route_rows(ids: torch.Tensor, experts: int, stream=None) -> RoutedRows:
         ids = _i32(ids, "ids")
         t, top_k = ids.shape
         capacity = sharq_route_rows_capacity(t, top_k, experts)
-        rows = torch.empty(capacity, dtype=torch.int32, device=ids.device)
-        offsets = torch.empty(experts + 1, dtype=torch.int32, device=ids.device)
-        slots = torch.empty((t, top_k), dtype=torch.int32, device=ids.device)
+        rows, offsets = ids.new_empty((capacity,)), ids.new_empty((experts + 1,))
+        slots = torch.empty_like(ids)
         sharq_route_rows(ids.data_ptr(), t, top_k, experts, rows.data_ptr(), capacity, offsets.data_ptr(),
                          slots.data_ptr())
     return RoutedRows(rows, offsets, slots)
@@ -638,7 +661,7 @@ def combine(y: torch.Tensor, slots: torch.Tensor, weights: torch.Tensor, add: to
     """out[t] = add[t] + sum_j weights[t, j] * y[slots[t, j]] (places with a slot below 0 are left out)."""
     if y.dim() != 2 or slots.dim() != 2:
         raise ValueError("y must be (rows, n), slots (t, top_k)")
-    _same_device(y, slots=slots, weights=weights, add=add, out=out)
+    _same_device(y, slots, weights, add, out)
     with _place(y, stream):
         t, top_k = slots.shape
         n = y.shape[1]
@@ -650,7 +673,7 @@ def combine(y: torch.Tensor, slots: torch.Tensor, weights: torch.Tensor, add: to
                 raise ValueError(f"add must be ({t}, {n}) of y's dtype")
             add = _aligned(add)
         if out is None:
-            out = torch.empty((t, n), dtype=out_dtype or y.dtype, device=y.device)
+            out = y.new_empty((t, n), dtype=out_dtype or y.dtype)
         elif tuple(out.shape) != (t, n) or not out.is_contiguous():
             raise ValueError(f"out must be a contiguous ({t}, {n}) tensor")
         y, weights = _aligned(y), weights.contiguous()

@@ -69,8 +69,8 @@ def test_quantize_gathered_rows(cuda_ok, fmt, dtype):
     _assert_matrix(sharq.quantize_fp4(to_dev(x, dtype), fmt, rows=rd), quantized(xr, fmt))
     for count in (0, 1, 100, 150, 1000):
         m = sharq.FP4Matrix(150, 224, fmt)
-        for b in (m.codes, m.scales):
-            b.fill_(0x22)
+        for part in (m.codes, m.scales):
+            part.fill_(0x22)
         m.row_scale.fill_(-1.0)
         sharq.quantize_fp4(to_dev(x, dtype), fmt, rows=rd, count=torch.tensor([count], dtype=torch.int32).cuda(), out=m)
         want = [a.copy() for a in quantized(xr, fmt)]
