@@ -21,17 +21,25 @@ struct Fp4Cfg {
   static constexpr int kChunks = BK / kVec / 4;  // 512-byte scale chunks per 128 rows and stage
   static constexpr int kNRB = BN / 128;          // 128-row blocks of weight scales, all in every CTA
   static constexpr int kWBytes = BNh * 128, kXBytes = BM * 128;
-  static constexpr int kSfx = kChunks * 512, kSfw = kNRB * kChunks * 512;
-  static constexpr int oW = 0, oX = oW + kWBytes, oSfx = oX + kXBytes, oSfw = oSfx + kSfx;
-  static constexpr int kStageBytes = ((oSfw + kSfw + 1023) / 1024) * 1024;
+  // a ring of operand stages of BK each
+  static constexpr int oW = 0, oX = oW + kWBytes, kStageBytes = oX + kXBytes;
   static constexpr int kStages = CTAS == 2 ? 5 : 4;
-  // tensor memory: accumulator, then a scale slot per stage
-  static constexpr int cSfx = 0, cSfw = 4 * kChunks, kSlotCols = 4 * (1 + kNRB) * kChunks;
+  // The scales go a step further, shared -> tensor memory, by warps whose waits
+  // and barriers cost more than the copy: they move two K tiles' worth at a
+  // time, in rings of their own in both memories.
+  static constexpr int kSfTiles = 2, kSfChunks = kSfTiles * kChunks;
+  static constexpr int kSfx = kSfChunks * 512, kSfw = kNRB * kSfChunks * 512;
+  static constexpr int oSfx = 0, oSfw = oSfx + kSfx, kSfBytes = oSfw + kSfw;
+  static constexpr int kSfStages = CTAS == 2 ? 3 : 2;
+  // tensor memory: accumulator, then the scale slots
+  static constexpr int cSfx = 0, cSfw = 4 * kSfChunks, kSlotCols = 4 * (1 + kNRB) * kSfChunks;
+  static constexpr int kSlots = 2;
+  static_assert(kNRB == 2 && kSfChunks % 4 == 0, "sixteen columns a store");
   static constexpr int kTmemCols = 512;
-  static_assert(BN + kStages * kSlotCols <= kTmemCols, "tensor memory budget");
-  static constexpr int kYRow = CTAS == 2 ? 64 : 32;   // bytes of an output row staged at a time, per warp
+  static_assert(BN + kSlots * kSlotCols <= kTmemCols, "tensor memory budget");
+  static constexpr int kYRow = CTAS == 2 ? 64 : 16;   // bytes of an output row staged at a time, per warp
   static constexpr int kYBuf = 8 * 32 * kYRow;
-  static constexpr int kSmemBytes = kStages * kStageBytes + kYBuf + 1024 /*align*/ + 256 /*barriers*/;
+  static constexpr int kSmemBytes = kStages * kStageBytes + kSfStages * kSfBytes + kYBuf + 8 * 128 * 4 + 1024 /*align*/ + 256 /*barriers*/;
   static_assert(kSmemBytes <= 232448, "shared memory budget");
   static constexpr uint32_t kIdesc = (1u << 7) | (1u << 10) | ((uint32_t)(BN >> 3) << 17) |
                                      ((KIND == GK_NVF4 ? 0u : 1u) << 23) | ((uint32_t)((BM * CTAS) >> 4) << 24);
@@ -66,27 +74,34 @@ __device__ __forceinline__ void fp4_mma(uint32_t d, uint64_t a, uint64_t b, uint
   }
 }
 
-// Per CTA (448 threads, one CTA per SM, persistent over output tiles):
-//   warp 0      TMA producer: activation and weight tiles (counted on the leader's
-//               full[]), this CTA's scale chunks (on its own sfull[]);
+// Per CTA (480 threads, one CTA per SM, persistent over output tiles):
+//   warp 0      TMA producer of activation and weight tiles (counted on the
+//               leader's full[]);
 //   warp 1      tensor memory; in the leader one thread issues the MMAs;
 //   warps 2-9   epilogue, two warps per 32-lane quadrant, 128 columns each;
-//   warps 10-13 scale chunks, shared memory -> the stage's tensor-memory slot.
+//   warps 10-13 scale chunks, shared memory -> the stage's tensor-memory slot;
+//   warp 14     producer of this CTA's scale chunks (sfull[]).
 // Every wait is bounded in time; a timeout sets the abort flag of both CTAs and
 // the device error word.
-template <int KIND, int CTAS, bool GROUPED>
-__global__ void __launch_bounds__(448, 1) gemm_fp4_kernel(const __grid_constant__ Fp4Maps maps, const Fp4GemmParams p) {
+// CTAS = 1 is the grouped form (expert segments are multiples of 128 rows, so two
+// row tiles need not share a weight), CTAS = 2 the plain one (32768 x 5120 x 5120
+// NVFP4: 362 us against 398 with one CTA a tile, and no size where it is slower).
+template <int KIND, int CTAS>
+__global__ void __launch_bounds__(480, 1) gemm_fp4_kernel(const __grid_constant__ Fp4Maps maps, const Fp4GemmParams p) {
   using C = Fp4Cfg<KIND, CTAS>;
-  static_assert(!GROUPED || CTAS == 1, "expert segments are multiples of 128 rows");
   constexpr bool kPair = CTAS == 2;
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
-  uint8_t* ybuf = smem + C::kStages * C::kStageBytes;
-  uint64_t* full = reinterpret_cast<uint64_t*>(ybuf + C::kYBuf);  // leader: both CTAs' tiles
+  uint8_t* sfbuf = smem + C::kStages * C::kStageBytes;
+  uint8_t* ybuf = sfbuf + C::kSfStages * C::kSfBytes;
+  float* rwbuf = reinterpret_cast<float*>(ybuf + C::kYBuf);        // the epilogue warps' column factors
+  uint64_t* full = reinterpret_cast<uint64_t*>(rwbuf + 8 * 128);   // leader: both CTAs' tiles
   uint64_t* empty = full + C::kStages;       // this CTA: the stage's MMAs have retired
   uint64_t* sfull = empty + C::kStages;      // this CTA: its scale chunks have landed
-  uint64_t* sf_ready = sfull + C::kStages;   // leader: both CTAs' scale slots are in tensor memory
-  uint64_t* acc_full = sf_ready + C::kStages;
+  uint64_t* sfree = sfull + C::kSfStages;    // this CTA: they have been copied
+  uint64_t* sf_ready = sfree + C::kSfStages; // leader: both CTAs' scale slots are in tensor memory
+  uint64_t* slot_empty = sf_ready + C::kSlots;  // this CTA: the slot's MMAs have retired
+  uint64_t* acc_full = slot_empty + C::kSlots;
   uint64_t* acc_empty = acc_full + 1;        // leader: both CTAs have drained their accumulator
   uint64_t* drain = acc_empty + 1;
   uint32_t* tmem_holder = reinterpret_cast<uint32_t*>(drain + 1);
@@ -100,8 +115,14 @@ __global__ void __launch_bounds__(448, 1) gemm_fp4_kernel(const __grid_constant_
     for (int s = 0; s < C::kStages; s++) {
       mbar_init(&full[s], 1);
       mbar_init(&empty[s], 1);
-      mbar_init(&sfull[s], 1);
+    }
+    for (int s = 0; s < C::kSlots; s++) {
       mbar_init(&sf_ready[s], 4 * CTAS);
+      mbar_init(&slot_empty[s], 1);
+    }
+    for (int s = 0; s < C::kSfStages; s++) {
+      mbar_init(&sfull[s], 1);
+      mbar_init(&sfree[s], 4);
     }
     mbar_init(acc_full, 1);
     mbar_init(acc_empty, 8 * CTAS);
@@ -144,11 +165,12 @@ __global__ void __launch_bounds__(448, 1) gemm_fp4_kernel(const __grid_constant_
   const int n_tiles = (int)((p.n + C::BN - 1) / C::BN);
   const int num_tiles = m_tiles * n_tiles;
   const int k_tiles = (int)((p.k + C::BK - 1) / C::BK);
+  const int k_groups = (k_tiles + C::kSfTiles - 1) / C::kSfTiles;  // of scales
   const int64_t s_blocks = (p.k / C::kVec + 3) / 4;  // 512-byte chunks per 128 rows
   const int64_t w_blocks = (p.n + 127) / 128, x_blocks = (p.t + 127) / 128;
   // expert of a row tile; -1 = rows outside every group
   auto tile_expert = [&](int64_t m0) -> int {
-    if constexpr (!GROUPED) return 0;
+    if constexpr (kPair) return 0;
     if (m0 >= (int64_t)__ldg(p.group_offsets + p.experts)) return -1;
     int lo = 0, hi = p.experts;  // off[lo] <= m0 < off[hi]
     while (hi - lo > 1) {
@@ -168,26 +190,15 @@ __global__ void __launch_bounds__(448, 1) gemm_fp4_kernel(const __grid_constant_
       for (int tile = cluster; tile < num_tiles && !*abort_flag; tile += nclusters) {
         const TileXY xy = tile_xy(tile, m_tiles, n_tiles, C::kBandTiles);
         const int64_t m0 = (int64_t)xy.mt * C::BM * CTAS + C::BM * (int64_t)rank;
-        const int e = tile_expert(m0);
+        const int e = tile_expert((int64_t)xy.mt * C::BM * CTAS);
         if (e < 0) continue;
         const int32_t wrow = (int32_t)(e * p.n + (int64_t)xy.nt * C::BN + C::BNh * (int64_t)rank);
-        // a block past the last one holds no row that is stored: any block stands in for its scales
-        const int64_t xb = m0 / 128 < x_blocks ? m0 / 128 : x_blocks - 1;
-        const uint8_t* g_sfx = p.sf_x + xb * s_blocks * 512;
-        const uint8_t* g_sfw[C::kNRB];
-#pragma unroll
-        for (int rb = 0; rb < C::kNRB; rb++) {
-          int64_t wb = (int64_t)xy.nt * C::kNRB + rb;
-          if (wb >= w_blocks) wb = w_blocks - 1;
-          g_sfw[rb] = p.sf_w + (e * w_blocks + wb) * s_blocks * 512;
-        }
         for (int kt = 0; kt < k_tiles; kt++, g++) {
           const int stage = (int)(g % C::kStages);
           const uint32_t ph = (g / C::kStages) & 1u;
           if (!mbar_wait(&empty[stage], ph ^ 1u, p.timeout_ns, abort_flag)) { give_up(); break; }
           const uint32_t sb = smem0 + (uint32_t)(stage * C::kStageBytes);
           const uint32_t fl = full_leader + (uint32_t)(stage * 8);
-          const uint32_t sf = smem_u32(&sfull[stage]);
           if (rank == 0) mbar_arrive_expect_tx_u32(smem_u32(&full[stage]), (uint32_t)(CTAS * (C::kWBytes + C::kXBytes)));
           if constexpr (kPair) {
             tma_load_2d_pair(sb + C::oW, &maps.w, kt * 128, wrow, fl);
@@ -196,34 +207,26 @@ __global__ void __launch_bounds__(448, 1) gemm_fp4_kernel(const __grid_constant_
             tma_load_2d_u32(sb + C::oW, &maps.w, kt * 128, wrow, fl);
             tma_load_2d_u32(sb + C::oX, &maps.x, kt * 128, (int32_t)m0, fl);
           }
-          const int64_t left = s_blocks - (int64_t)kt * C::kChunks;
-          const uint32_t bytes = (uint32_t)(left < C::kChunks ? left : C::kChunks) * 512u;
-          const int64_t so = (int64_t)kt * C::kChunks * 512;
-          mbar_arrive_expect_tx_u32(sf, bytes * (1 + C::kNRB));
-          bulk_load_u32(sb + C::oSfx, g_sfx + so, bytes, sf);
-#pragma unroll
-          for (int rb = 0; rb < C::kNRB; rb++)
-            bulk_load_u32(sb + C::oSfw + rb * C::kChunks * 512, g_sfw[rb] + so, bytes, sf);
           issued |= 1u << stage;
           issued_par = (issued_par & ~(1u << stage)) | (ph << stage);
         }
       }
       if (*abort_flag) {
-        // let every load already issued land before the block can exit
+        // let every load already issued land before the block can exit (the pair's are all counted here)
         for (int i = 0; i < C::kStages; i++)
-          if ((issued >> i) & 1u) {
-            (void)mbar_wait(&sfull[i], (issued_par >> i) & 1u, 1000000000ull, nullptr, true);
-            if (rank == 0) (void)mbar_wait(&full[i], (issued_par >> i) & 1u, 1000000000ull, nullptr, true);
-          }
+          if (rank == 0 && ((issued >> i) & 1u)) (void)mbar_wait(&full[i], (issued_par >> i) & 1u, 1000000000ull, nullptr, true);
       }
     }
   } else if (warp == 1) {
     // ------------------------------------------------------------------ MMA
-    if (rank == 0 && lane == 0) {
-      uint32_t g = 0;
-      int it = 0;
+    // the whole warp runs the loop, so that its addresses and descriptors stay
+    // uniform; one lane issues (a branch on the lane number cost 112 cycles an
+    // MMA in moves to uniform registers, more than the MMA's own 124 leave room for)
+    if (rank == 0) {
+      uint32_t stage = 0, ph = 0, slot = 0, sph = 0, acc_ph = 1;
       constexpr uint32_t kHi128 = desc_hi(1024, 2), kLbo = 1u << 16;
-      const uint32_t lo0 = smem_u32(smem) >> 4;
+      const uint32_t lo0 = __shfl_sync(0xffffffffu, smem_u32(smem) >> 4, 0);
+      const uint32_t tm = __shfl_sync(0xffffffffu, tmem_base, 0);
       auto commit = [&](uint64_t* bar) {
         if constexpr (kPair) {
           tc_commit_pair(smem_u32(bar));
@@ -235,41 +238,61 @@ __global__ void __launch_bounds__(448, 1) gemm_fp4_kernel(const __grid_constant_
       for (int tile = cluster; tile < num_tiles && !*abort_flag; tile += nclusters) {
         const TileXY xy = tile_xy(tile, m_tiles, n_tiles, C::kBandTiles);
         if (tile_expert((int64_t)xy.mt * C::BM * CTAS) < 0) continue;
-        if (!mbar_wait(acc_empty, (uint32_t)(it & 1) ^ 1u, p.timeout_ns, abort_flag)) { give_up(); break; }
-        it++;
+        if (!mbar_wait(acc_empty, acc_ph, p.timeout_ns, abort_flag)) { give_up(); break; }
+        acc_ph ^= 1u;
         tc_fence_after();
+        int left = (int)((p.k + 63) / 64);  // MMAs of this tile still to come (beyond K there are no scales)
         uint32_t accumulate = 0;
-        for (int kt = 0; kt < k_tiles; kt++, g++) {
-          const int stage = (int)(g % C::kStages);
-          const uint32_t ph = (g / C::kStages) & 1u;
-          if (!mbar_wait(&full[stage], ph, p.timeout_ns, abort_flag)) { give_up(); break; }
-          if (!mbar_wait(&sf_ready[stage], ph, p.timeout_ns, abort_flag)) { give_up(); break; }
+        bool ok = true;
+        for (int kt = 0; kt < k_tiles; kt++) {
+          const uint32_t half = (uint32_t)kt % C::kSfTiles;
+          ok = mbar_wait(&full[stage], ph, p.timeout_ns, abort_flag);
+          if (half == 0) ok = ok && mbar_wait(&sf_ready[slot], sph, p.timeout_ns, abort_flag);
+          if (!ok) break;
           tc_fence_after();
-          const uint32_t ls = lo0 + (uint32_t)(stage * (C::kStageBytes >> 4));
-          const uint32_t sl = tmem_base + C::BN + (uint32_t)(stage * C::kSlotCols);
-          const int64_t left = p.k - (int64_t)kt * C::BK;
+          const uint32_t ls = lo0 + stage * (uint32_t)(C::kStageBytes >> 4);
+          const uint32_t sl = tm + C::BN + slot * (uint32_t)C::kSlotCols;
+          const uint32_t slx = sl + C::cSfx + 4 * C::kChunks * half;
+          const uint32_t slw = sl + C::cSfw + 4 * C::kNRB * C::kChunks * half;
+          const bool last = half == C::kSfTiles - 1 || kt == k_tiles - 1;
+          if (elect_one()) {
 #pragma unroll
-          for (int kb = 0; kb < C::BK / 64; kb++) {
-            if (64 * kb < left) {  // beyond K there are no scales
-              constexpr int kScales = 64 / C::kVec;
-              const uint32_t chunk = (kb * kScales) / 4, byte = (kb * kScales) % 4;
-              const uint32_t idesc = C::kIdesc | (byte << 29) | (byte << 4);
-              const uint64_t a = desc_lohi((ls + (C::oX >> 4) + 2 * kb) | kLbo, kHi128);
-              const uint64_t b = desc_lohi((ls + (C::oW >> 4) + 2 * kb) | kLbo, kHi128);
-              const uint32_t sfa = (sl + C::cSfx + 4 * chunk) | (byte << 30);
-              const uint32_t sfb = (sl + C::cSfw + 4 * C::kNRB * chunk) | (byte << 30);
-              fp4_mma<KIND, CTAS>(tmem_base, a, b, idesc, sfa, sfb, accumulate);
-              accumulate = 1;
+            for (int kb = 0; kb < C::BK / 64; kb++) {
+              if (kb < left) {
+                constexpr int kScales = 64 / C::kVec;
+                const uint32_t chunk = (kb * kScales) / 4, byte = (kb * kScales) % 4;
+                const uint32_t idesc = C::kIdesc | (byte << 29) | (byte << 4);
+                const uint64_t a = desc_lohi((ls + (C::oX >> 4) + 2 * kb) | kLbo, kHi128);
+                const uint64_t b = desc_lohi((ls + (C::oW >> 4) + 2 * kb) | kLbo, kHi128);
+                const uint32_t sfa = (slx + 4 * chunk) | (byte << 30);
+                const uint32_t sfb = (slw + 4 * C::kNRB * chunk) | (byte << 30);
+                fp4_mma<KIND, CTAS>(tm, a, b, idesc, sfa, sfb, kb == 0 ? accumulate : 1u);
+              }
             }
+            commit(&empty[stage]);
+            if (last) commit(&slot_empty[slot]);
+            if (kt == k_tiles - 1) commit(acc_full);
           }
-          commit(&empty[stage]);
+          __syncwarp();
+          accumulate = 1;
+          left -= C::BK / 64;
+          if (++stage == C::kStages) {
+            stage = 0;
+            ph ^= 1u;
+          }
+          if (last && ++slot == C::kSlots) {
+            slot = 0;
+            sph ^= 1u;
+          }
         }
-        if (*abort_flag) break;
-        commit(acc_full);
+        if (!ok) { give_up(); break; }
       }
       // every MMA is complete before either CTA frees tensor memory or exits
-      if constexpr (kPair) tc_commit_pair(smem_u32(drain));
-      else tc_commit(drain);
+      if (elect_one()) {
+        if constexpr (kPair) tc_commit_pair(smem_u32(drain));
+        else tc_commit(drain);
+      }
+      __syncwarp();
       (void)mbar_wait(drain, 0, 1000000000ull, nullptr, true);
     }
   } else if (warp < 10) {
@@ -289,68 +312,132 @@ __global__ void __launch_bounds__(448, 1) gemm_fp4_kernel(const __grid_constant_
       const int64_t row = m0 + 32 * q + lane;
       const float rx = row < p.t ? __ldg(p.row_x + row) : 0.0f;
       const int64_t n0 = (int64_t)xy.nt * C::BN + kCols * hcol;
-      const float* rw = p.row_w + e * p.n;
+      // this warp's 128 column factors, one lane's four at a time (n is a multiple of 8)
+      float* rws = rwbuf + (warp - 2) * kCols;
+      __syncwarp();  // the previous tile's have been read
+      const int64_t cw = n0 + 4 * lane;
+      *reinterpret_cast<float4*>(rws + 4 * lane) =
+          cw < p.n ? __ldg(reinterpret_cast<const float4*>(p.row_w + e * p.n + cw)) : make_float4(0.f, 0.f, 0.f, 0.f);
+      __syncwarp();
       if (!mbar_wait(acc_full, (uint32_t)(it & 1), p.timeout_ns, abort_flag)) { give_up(); break; }
       it++;
       tc_fence_after();
       const int32_t row0 = (int32_t)(row - lane);
+      // kYRow bytes of each row at a time through shared memory, written by TMA
+      // stores (whole lines; rows at or beyond t and columns from n on are clipped)
+      auto store = [&](const uint32_t* w, int64_t col) {  // kYRow / 4 words of each lane's row
+        if (lane == 0) bulk_wait_group_read0();  // the previous store has read the buffer
+        __syncwarp();
+        uint4* d = reinterpret_cast<uint4*>(yb + C::kYRow * lane);
+#pragma unroll
+        for (int j = 0; j < C::kYRow / 16; j++) d[j] = make_uint4(w[4 * j], w[4 * j + 1], w[4 * j + 2], w[4 * j + 3]);
+        fence_proxy_async_smem();
+        __syncwarp();
+        if (lane == 0 && col < p.n) {
+          tma_store_2d(&maps.y, smem_u32(yb), (int32_t)((p.y_bf16 ? 2 : 4) * col), row0);
+          bulk_commit_group();
+        }
+      };
+      // 32 columns times the row factors; they were read while the tile's MMAs ran
+      auto scaled = [&](const uint32_t (&v)[32], int c, float (&f)[32]) {
+#pragma unroll
+        for (int j = 0; j < 8; j++) {
+          const float4 s = *reinterpret_cast<const float4*>(rws + 32 * c + 4 * j);
+          f[4 * j] = __fmul_rn(__fmul_rn(__uint_as_float(v[4 * j]), rx), s.x);
+          f[4 * j + 1] = __fmul_rn(__fmul_rn(__uint_as_float(v[4 * j + 1]), rx), s.y);
+          f[4 * j + 2] = __fmul_rn(__fmul_rn(__uint_as_float(v[4 * j + 2]), rx), s.z);
+          f[4 * j + 3] = __fmul_rn(__fmul_rn(__uint_as_float(v[4 * j + 3]), rx), s.w);
+        }
+      };
+      if (p.y_bf16) {
+        // all columns into registers as bf16, then the accumulator is released and
+        // the next tile's MMAs run under the stores
+        uint32_t pk[kCols / 2];
+#pragma unroll
+        for (int c2 = 0; c2 < kCols / 32; c2 += 2) {
+          uint32_t v[2][32];  // two loads in flight per wait
+          tmem_ld32_nowait(tq + (uint32_t)(32 * c2), v[0]);
+          tmem_ld32_nowait(tq + (uint32_t)(32 * c2 + 32), v[1]);
+          tmem_ld_wait();
+#pragma unroll
+          for (int h = 0; h < 2; h++) {
+            float f[32];
+            scaled(v[h], c2 + h, f);
+#pragma unroll
+            for (int j = 0; j < 16; j++) {
+              const __nv_bfloat162 h2 = __floats2bfloat162_rn(f[2 * j], f[2 * j + 1]);
+              pk[16 * (c2 + h) + j] = *reinterpret_cast<const uint32_t*>(&h2);
+            }
+          }
+        }
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) arrive_leader(acc_empty_leader);
+        if (row0 >= p.t) continue;
+#pragma unroll
+        for (int i = 0; i < kCols / 2; i += C::kYRow / 4) store(pk + i, n0 + 2 * i);
+        continue;
+      }
 #pragma unroll 1
       for (int c = 0; c < kCols / 32; c++) {
         uint32_t v[32];
         tmem_ld32_nowait(tq + (uint32_t)(32 * c), v);
         tmem_ld_wait();
         float f[32];
-#pragma unroll
-        for (int j = 0; j < 8; j++) {  // n is a multiple of 8: four columns are inside or outside together
-          const int64_t col = n0 + 32 * c + 4 * j;
-          const float4 s = col < p.n ? __ldg(reinterpret_cast<const float4*>(rw + col)) : make_float4(0.f, 0.f, 0.f, 0.f);
-          f[4 * j] = __fmul_rn(__fmul_rn(__uint_as_float(v[4 * j]), rx), s.x);
-          f[4 * j + 1] = __fmul_rn(__fmul_rn(__uint_as_float(v[4 * j + 1]), rx), s.y);
-          f[4 * j + 2] = __fmul_rn(__fmul_rn(__uint_as_float(v[4 * j + 2]), rx), s.z);
-          f[4 * j + 3] = __fmul_rn(__fmul_rn(__uint_as_float(v[4 * j + 3]), rx), s.w);
-        }
-        if (c == kCols / 32 - 1) {
-          tc_fence_before();
-          __syncwarp();
-          if (lane == 0) arrive_leader(acc_empty_leader);
-        }
+        scaled(v, c, f);
         if (row0 >= p.t) continue;
-        // kYRow bytes of each row at a time through shared memory, written by TMA
-        // stores (whole lines; rows at or beyond t and columns from n on are clipped)
-        const int es = p.y_bf16 ? 2 : 4, per = C::kYRow / es;
 #pragma unroll
-        for (int h = 0; h < 32 * 4 / C::kYRow; h++) {
-          if (p.y_bf16 && h >= 32 * 2 / C::kYRow) break;
-          if (lane == 0) bulk_wait_group_read0();  // the previous store has read the buffer
-          __syncwarp();
-          uint4* d = reinterpret_cast<uint4*>(yb + C::kYRow * lane);
+        for (int i = 0; i < 32; i++) v[i] = __float_as_uint(f[i]);
 #pragma unroll
-          for (int j = 0; j < C::kYRow / 16; j++) {
-            uint32_t o[4];
-            if (p.y_bf16) {
-#pragma unroll
-              for (int i = 0; i < 4; i++) {
-                const int at = (h * (C::kYRow / 2) + 8 * j + 2 * i) & 31;
-                const __nv_bfloat162 h2 = __floats2bfloat162_rn(f[at], f[at + 1]);
-                o[i] = *reinterpret_cast<const uint32_t*>(&h2);
-              }
-            } else {
-#pragma unroll
-              for (int i = 0; i < 4; i++) o[i] = __float_as_uint(f[h * (C::kYRow / 4) + 4 * j + i]);
-            }
-            d[j] = make_uint4(o[0], o[1], o[2], o[3]);
-          }
-          fence_proxy_async_smem();
-          __syncwarp();
-          const int64_t col = n0 + 32 * c + h * per;
-          if (lane == 0 && col < p.n) {
-            tma_store_2d(&maps.y, smem_u32(yb), (int32_t)(es * col), row0);
-            bulk_commit_group();
-          }
-        }
+        for (int i = 0; i < 32; i += C::kYRow / 4) store(v + i, n0 + 32 * c + i);
       }
+      tc_fence_before();
+      __syncwarp();
+      if (lane == 0) arrive_leader(acc_empty_leader);
     }
     if (lane == 0) bulk_wait_group0();  // output stores complete
+  } else if (warp == 14) {
+    // ------------------------------------------------------ scale producer
+    if (lane == 0) {
+      uint32_t g = 0, issued = 0, issued_par = 0;
+      const uint32_t sf0 = smem_u32(sfbuf);
+      for (int tile = cluster; tile < num_tiles && !*abort_flag; tile += nclusters) {
+        const TileXY xy = tile_xy(tile, m_tiles, n_tiles, C::kBandTiles);
+        const int64_t m0 = (int64_t)xy.mt * C::BM * CTAS + C::BM * (int64_t)rank;
+        const int e = tile_expert((int64_t)xy.mt * C::BM * CTAS);
+        if (e < 0) continue;
+        // a block past the last one holds no row that is stored: any block stands in for its scales
+        const int64_t xb = m0 / 128 < x_blocks ? m0 / 128 : x_blocks - 1;
+        const uint8_t* g_sfx = p.sf_x + xb * s_blocks * 512;
+        const uint8_t* g_sfw[C::kNRB];
+#pragma unroll
+        for (int rb = 0; rb < C::kNRB; rb++) {
+          int64_t wb = (int64_t)xy.nt * C::kNRB + rb;
+          if (wb >= w_blocks) wb = w_blocks - 1;
+          g_sfw[rb] = p.sf_w + (e * w_blocks + wb) * s_blocks * 512;
+        }
+        for (int q = 0; q < k_groups; q++, g++) {
+          const int ss = (int)(g % C::kSfStages);
+          const uint32_t ph = (g / C::kSfStages) & 1u;
+          if (!mbar_wait(&sfree[ss], ph ^ 1u, p.timeout_ns, abort_flag)) { give_up(); break; }
+          const uint32_t sb = sf0 + (uint32_t)(ss * C::kSfBytes), sf = smem_u32(&sfull[ss]);
+          const int64_t left = s_blocks - (int64_t)q * C::kSfChunks;
+          const uint32_t bytes = (uint32_t)(left < C::kSfChunks ? left : C::kSfChunks) * 512u;
+          const int64_t so = (int64_t)q * C::kSfChunks * 512;
+          mbar_arrive_expect_tx_u32(sf, bytes * (1 + C::kNRB));
+          bulk_load_u32(sb + C::oSfx, g_sfx + so, bytes, sf);
+#pragma unroll
+          for (int rb = 0; rb < C::kNRB; rb++)
+            bulk_load_u32(sb + C::oSfw + rb * C::kSfChunks * 512, g_sfw[rb] + so, bytes, sf);
+          issued |= 1u << ss;
+          issued_par = (issued_par & ~(1u << ss)) | (ph << ss);
+        }
+      }
+      if (*abort_flag) {
+        for (int i = 0; i < C::kSfStages; i++)
+          if ((issued >> i) & 1u) (void)mbar_wait(&sfull[i], (issued_par >> i) & 1u, 1000000000ull, nullptr, true);
+      }
+    }
   } else {
     // ------------------------------------------------ scale-slot staging
     const int q = warp & 3;
@@ -360,25 +447,33 @@ __global__ void __launch_bounds__(448, 1) gemm_fp4_kernel(const __grid_constant_
     for (int tile = cluster; tile < num_tiles && !*abort_flag; tile += nclusters) {
       const TileXY xy = tile_xy(tile, m_tiles, n_tiles, C::kBandTiles);
       if (tile_expert((int64_t)xy.mt * C::BM * CTAS) < 0) continue;
-      for (int kt = 0; kt < k_tiles; kt++, g++) {
-        const int stage = (int)(g % C::kStages);
-        // the chunks were loaded into a stage, and so into a slot, whose MMAs have retired
-        if (!mbar_wait(&sfull[stage], (g / C::kStages) & 1u, p.timeout_ns, abort_flag)) { give_up(); break; }
-        tc_fence_after();
-        const uint8_t* sb = smem + stage * C::kStageBytes;
-        const uint32_t st = tq + C::BN + (uint32_t)(stage * C::kSlotCols);
+      for (int kq = 0; kq < k_groups; kq++, g++) {
+        const uint32_t ss = g % C::kSfStages, slot = g % C::kSlots;
+        if (!mbar_wait(&sfull[ss], (g / C::kSfStages) & 1u, p.timeout_ns, abort_flag)) { give_up(); break; }
+        const uint8_t* sb = sfbuf + ss * C::kSfBytes + 16 * lane;
+        uint4 x[C::kSfChunks], wv[C::kNRB * C::kSfChunks];
 #pragma unroll
-        for (int c = 0; c < C::kChunks; c++) {
-          tmem_st4(st + C::cSfx + 4 * c, *reinterpret_cast<const uint4*>(sb + C::oSfx + 512 * c + 16 * lane));
+        for (int c = 0; c < C::kSfChunks; c++) {
+          x[c] = *reinterpret_cast<const uint4*>(sb + C::oSfx + 512 * c);
 #pragma unroll
           for (int rb = 0; rb < C::kNRB; rb++)
-            tmem_st4(st + C::cSfw + 4 * C::kNRB * c + 4 * rb,
-                     *reinterpret_cast<const uint4*>(sb + C::oSfw + (rb * C::kChunks + c) * 512 + 16 * lane));
+            wv[C::kNRB * c + rb] = *reinterpret_cast<const uint4*>(sb + C::oSfw + (rb * C::kSfChunks + c) * 512);
         }
+        // the MMAs that used the slot before have retired
+        if (!mbar_wait(&slot_empty[slot], ((g / C::kSlots) & 1u) ^ 1u, p.timeout_ns, abort_flag)) { give_up(); break; }
+        tc_fence_after();
+        const uint32_t st = tq + C::BN + slot * (uint32_t)C::kSlotCols;
+#pragma unroll
+        for (int c = 0; c < C::kSfChunks; c += 4) tmem_st16(st + C::cSfx + 4 * c, x + c);
+#pragma unroll
+        for (int c = 0; c < C::kNRB * C::kSfChunks; c += 4) tmem_st16(st + C::cSfw + 4 * c, wv + c);
         tmem_st_wait();
         tc_fence_before();
         __syncwarp();
-        if (lane == 0) arrive_leader(ready_leader + (uint32_t)(stage * 8));
+        if (lane == 0) {
+          arrive_leader(ready_leader + slot * 8);
+          mbar_arrive(&sfree[ss]);
+        }
       }
     }
   }

@@ -824,11 +824,11 @@ Fp4Params fp4_params(const void* x, int64_t x_rows, int64_t stride, const int32_
   return fp;
 }
 
-template <int KIND, int CTAS, bool GROUPED>
+template <int KIND, int CTAS>
 sharq_status launch_gemm_fp4(const sharq_fp4* x, const sharq_fp4* w, const int32_t* offsets, void* y, sharq_dtype y_dt,
                              cudaStream_t s) {
   using C = Fp4Cfg<KIND, CTAS>;
-  sharq_status st = ensure_smem_limit<gemm_fp4_kernel<KIND, CTAS, GROUPED>>(C::kSmemBytes);
+  sharq_status st = ensure_smem_limit<gemm_fp4_kernel<KIND, CTAS>>(C::kSmemBytes);
   if (st != SHARQ_OK) return st;
   const int64_t t = x->rows, n = w->rows, k = x->k, es = y_dt == SHARQ_BF16 ? 2 : 4;
   Fp4Maps maps;
@@ -855,7 +855,7 @@ sharq_status launch_gemm_fp4(const sharq_fp4* x, const sharq_fp4* w, const int32
   const int64_t tiles = ((t + C::BM * CTAS - 1) / (C::BM * CTAS)) * ((n + C::BN - 1) / C::BN);
   if (tiles > INT32_MAX / 2) return fail(SHARQ_ERR_UNSUPPORTED, "%lld output tiles", (long long)tiles);
   const int64_t slots = sm_count() / CTAS;
-  return launch_ex(gemm_fp4_kernel<KIND, CTAS, GROUPED>, dim3((unsigned)(CTAS * (tiles < slots ? tiles : slots))), dim3(448),
+  return launch_ex(gemm_fp4_kernel<KIND, CTAS>, dim3((unsigned)(CTAS * (tiles < slots ? tiles : slots))), dim3(480),
                    C::kSmemBytes, s, CTAS, maps, gp);
 }
 
@@ -876,10 +876,10 @@ sharq_status run_linear_fp4(const sharq_fp4* x, const sharq_fp4* w, const int32_
   st = check_dtype(y_dt, "y");
   if (st != SHARQ_OK) return st;
   if (offsets)
-    return x->fmt == SHARQ_NVFP4 ? launch_gemm_fp4<GK_NVF4, 1, true>(x, w, offsets, y, y_dt, s)
-                                 : launch_gemm_fp4<GK_MXF4, 1, true>(x, w, offsets, y, y_dt, s);
-  return x->fmt == SHARQ_NVFP4 ? launch_gemm_fp4<GK_NVF4, 1, false>(x, w, nullptr, y, y_dt, s)
-                               : launch_gemm_fp4<GK_MXF4, 1, false>(x, w, nullptr, y, y_dt, s);
+    return x->fmt == SHARQ_NVFP4 ? launch_gemm_fp4<GK_NVF4, 1>(x, w, offsets, y, y_dt, s)
+                                 : launch_gemm_fp4<GK_MXF4, 1>(x, w, offsets, y, y_dt, s);
+  return x->fmt == SHARQ_NVFP4 ? launch_gemm_fp4<GK_NVF4, 2>(x, w, nullptr, y, y_dt, s)
+                               : launch_gemm_fp4<GK_MXF4, 2>(x, w, nullptr, y, y_dt, s);
 }
 
 template <int VPL>
