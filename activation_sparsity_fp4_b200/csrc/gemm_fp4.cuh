@@ -34,7 +34,7 @@ struct Fp4Cfg {
   // tensor memory: accumulator, then the scale slots
   static constexpr int cSfx = 0, cSfw = 4 * kSfChunks, kSlotCols = 4 * (1 + kNRB) * kSfChunks;
   static constexpr int kSlots = 2;
-  static_assert(kNRB == 2 && kSfChunks % 4 == 0, "sixteen columns a store");
+  static_assert(kNRB == 2, "256 weight rows");
   static constexpr int kTmemCols = 512;
   static_assert(BN + kSlots * kSlotCols <= kTmemCols, "tensor memory budget");
   static constexpr int kYRow = CTAS == 2 ? 64 : 16;   // bytes of an output row staged at a time, per warp
@@ -45,6 +45,11 @@ struct Fp4Cfg {
                                      ((KIND == GK_NVF4 ? 0u : 1u) << 23) | ((uint32_t)((BM * CTAS) >> 4) << 24);
   static constexpr int kBandTiles = 2048 / (BM * CTAS);  // row tiles per raster band
 };
+
+// 128 registers a thread at launch; the epilogue's two warpgroups hold 128 sums
+// and more, the other two give up what they can spare.
+constexpr int kFp4GemmThreads = 512, kFp4GemmRegs = 128, kFp4RegsLow = 72, kFp4RegsHigh = 184;
+static_assert(2 * kFp4RegsLow + 2 * kFp4RegsHigh == 4 * kFp4GemmRegs, "no more than the block was launched with");
 
 struct Fp4Maps {
   CUtensorMap x, w, y;
@@ -74,20 +79,23 @@ __device__ __forceinline__ void fp4_mma(uint32_t d, uint64_t a, uint64_t b, uint
   }
 }
 
-// Per CTA (480 threads, one CTA per SM, persistent over output tiles):
+// Per CTA (512 threads, one CTA per SM, persistent over output tiles):
 //   warp 0      TMA producer of activation and weight tiles (counted on the
 //               leader's full[]);
-//   warp 1      tensor memory; in the leader one thread issues the MMAs;
-//   warps 2-9   epilogue, two warps per 32-lane quadrant, 128 columns each;
-//   warps 10-13 scale chunks, shared memory -> the stage's tensor-memory slot;
-//   warp 14     producer of this CTA's scale chunks (sfull[]).
+//   warp 1      tensor memory; in the leader it issues the MMAs;
+//   warp 2      producer of this CTA's scale chunks (sfull[]); warp 3 has no part;
+//   warps 4-7   scale chunks, shared memory -> a tensor-memory slot;
+//   warps 8-15  epilogue, two warps per 32-lane quadrant, 128 columns each: the
+//               raw sums into registers, so that the next tile's MMAs wait for
+//               the tensor-memory loads alone; the factors, the rounding and the
+//               stores run under those MMAs.
 // Every wait is bounded in time; a timeout sets the abort flag of both CTAs and
 // the device error word.
 // CTAS = 1 is the grouped form (expert segments are multiples of 128 rows, so two
 // row tiles need not share a weight), CTAS = 2 the plain one (32768 x 5120 x 5120
 // NVFP4: 362 us against 398 with one CTA a tile, and no size where it is slower).
 template <int KIND, int CTAS>
-__global__ void __launch_bounds__(480, 1) gemm_fp4_kernel(const __grid_constant__ Fp4Maps maps, const Fp4GemmParams p) {
+__global__ void __launch_bounds__(kFp4GemmThreads, 1) gemm_fp4_kernel(const __grid_constant__ Fp4Maps maps, const Fp4GemmParams p) {
   using C = Fp4Cfg<KIND, CTAS>;
   constexpr bool kPair = CTAS == 2;
   extern __shared__ uint8_t smem_raw[];
@@ -181,6 +189,7 @@ __global__ void __launch_bounds__(480, 1) gemm_fp4_kernel(const __grid_constant_
     return lo;
   };
 
+  if (warp < 4) regs_down<kFp4RegsLow>();
   if (warp == 0) {
     // ------------------------------------------------------------- producer
     if (lane == 0) {
@@ -228,12 +237,8 @@ __global__ void __launch_bounds__(480, 1) gemm_fp4_kernel(const __grid_constant_
       const uint32_t lo0 = __shfl_sync(0xffffffffu, smem_u32(smem) >> 4, 0);
       const uint32_t tm = __shfl_sync(0xffffffffu, tmem_base, 0);
       auto commit = [&](uint64_t* bar) {
-        if constexpr (kPair) {
-          tc_commit_pair(smem_u32(bar));
-          tc_commit_pair(mapa_u32(smem_u32(bar), 1));
-        } else {
-          tc_commit(bar);
-        }
+        if constexpr (kPair) tc_commit_pair_both(smem_u32(bar));
+        else tc_commit(bar);
       };
       for (int tile = cluster; tile < num_tiles && !*abort_flag; tile += nclusters) {
         const TileXY xy = tile_xy(tile, m_tiles, n_tiles, C::kBandTiles);
@@ -295,14 +300,15 @@ __global__ void __launch_bounds__(480, 1) gemm_fp4_kernel(const __grid_constant_
       __syncwarp();
       (void)mbar_wait(drain, 0, 1000000000ull, nullptr, true);
     }
-  } else if (warp < 10) {
+  } else if (warp >= 8) {
+    regs_up<kFp4RegsHigh>();
     // ------------------------------------------------------------- epilogue
     // accumulator lanes 32q..32q+31 (output rows), columns 128h..128h+127
     constexpr int kCols = C::BN / 2;
-    const int q = warp & 3, hcol = (warp - 2) >> 2;
+    const int q = warp & 3, hcol = (warp - 8) >> 2;
     const uint32_t tq = tmem_base + ((uint32_t)(32 * q) << 16) + (uint32_t)(kCols * hcol);
     const uint32_t acc_empty_leader = at_leader(smem_u32(acc_empty));
-    uint8_t* yb = ybuf + (warp - 2) * 32 * C::kYRow;
+    uint8_t* yb = ybuf + (warp - 8) * 32 * C::kYRow;
     int it = 0;
     for (int tile = cluster; tile < num_tiles && !*abort_flag; tile += nclusters) {
       const TileXY xy = tile_xy(tile, m_tiles, n_tiles, C::kBandTiles);
@@ -313,7 +319,7 @@ __global__ void __launch_bounds__(480, 1) gemm_fp4_kernel(const __grid_constant_
       const float rx = row < p.t ? __ldg(p.row_x + row) : 0.0f;
       const int64_t n0 = (int64_t)xy.nt * C::BN + kCols * hcol;
       // this warp's 128 column factors, one lane's four at a time (n is a multiple of 8)
-      float* rws = rwbuf + (warp - 2) * kCols;
+      float* rws = rwbuf + (warp - 8) * kCols;
       __syncwarp();  // the previous tile's have been read
       const int64_t cw = n0 + 4 * lane;
       *reinterpret_cast<float4*>(rws + 4 * lane) =
@@ -338,65 +344,38 @@ __global__ void __launch_bounds__(480, 1) gemm_fp4_kernel(const __grid_constant_
           bulk_commit_group();
         }
       };
-      // 32 columns times the row factors; they were read while the tile's MMAs ran
-      auto scaled = [&](const uint32_t (&v)[32], int c, float (&f)[32]) {
+      uint32_t v[kCols];
 #pragma unroll
-        for (int j = 0; j < 8; j++) {
-          const float4 s = *reinterpret_cast<const float4*>(rws + 32 * c + 4 * j);
-          f[4 * j] = __fmul_rn(__fmul_rn(__uint_as_float(v[4 * j]), rx), s.x);
-          f[4 * j + 1] = __fmul_rn(__fmul_rn(__uint_as_float(v[4 * j + 1]), rx), s.y);
-          f[4 * j + 2] = __fmul_rn(__fmul_rn(__uint_as_float(v[4 * j + 2]), rx), s.z);
-          f[4 * j + 3] = __fmul_rn(__fmul_rn(__uint_as_float(v[4 * j + 3]), rx), s.w);
-        }
-      };
-      if (p.y_bf16) {
-        // all columns into registers as bf16, then the accumulator is released and
-        // the next tile's MMAs run under the stores
-        uint32_t pk[kCols / 2];
-#pragma unroll
-        for (int c2 = 0; c2 < kCols / 32; c2 += 2) {
-          uint32_t v[2][32];  // two loads in flight per wait
-          tmem_ld32_nowait(tq + (uint32_t)(32 * c2), v[0]);
-          tmem_ld32_nowait(tq + (uint32_t)(32 * c2 + 32), v[1]);
-          tmem_ld_wait();
-#pragma unroll
-          for (int h = 0; h < 2; h++) {
-            float f[32];
-            scaled(v[h], c2 + h, f);
-#pragma unroll
-            for (int j = 0; j < 16; j++) {
-              const __nv_bfloat162 h2 = __floats2bfloat162_rn(f[2 * j], f[2 * j + 1]);
-              pk[16 * (c2 + h) + j] = *reinterpret_cast<const uint32_t*>(&h2);
-            }
-          }
-        }
-        tc_fence_before();
-        __syncwarp();
-        if (lane == 0) arrive_leader(acc_empty_leader);
-        if (row0 >= p.t) continue;
-#pragma unroll
-        for (int i = 0; i < kCols / 2; i += C::kYRow / 4) store(pk + i, n0 + 2 * i);
-        continue;
-      }
-#pragma unroll 1
-      for (int c = 0; c < kCols / 32; c++) {
-        uint32_t v[32];
-        tmem_ld32_nowait(tq + (uint32_t)(32 * c), v);
-        tmem_ld_wait();
-        float f[32];
-        scaled(v, c, f);
-        if (row0 >= p.t) continue;
-#pragma unroll
-        for (int i = 0; i < 32; i++) v[i] = __float_as_uint(f[i]);
-#pragma unroll
-        for (int i = 0; i < 32; i += C::kYRow / 4) store(v + i, n0 + 32 * c + i);
-      }
+      for (int c = 0; c < kCols / 32; c++)
+        tmem_ld32_nowait(tq + (uint32_t)(32 * c), *reinterpret_cast<uint32_t(*)[32]>(v + 32 * c));
+      tmem_ld_wait();
       tc_fence_before();
       __syncwarp();
       if (lane == 0) arrive_leader(acc_empty_leader);
+      if (row0 >= p.t) continue;
+#pragma unroll
+      for (int c = 0; c < kCols; c += 4) {  // times the row factors, read while the tile's MMAs ran
+        const float4 s = *reinterpret_cast<const float4*>(rws + c);
+        v[c] = __float_as_uint(__fmul_rn(__fmul_rn(__uint_as_float(v[c]), rx), s.x));
+        v[c + 1] = __float_as_uint(__fmul_rn(__fmul_rn(__uint_as_float(v[c + 1]), rx), s.y));
+        v[c + 2] = __float_as_uint(__fmul_rn(__fmul_rn(__uint_as_float(v[c + 2]), rx), s.z));
+        v[c + 3] = __float_as_uint(__fmul_rn(__fmul_rn(__uint_as_float(v[c + 3]), rx), s.w));
+      }
+      if (p.y_bf16) {
+#pragma unroll
+        for (int i = 0; i < kCols / 2; i++) {
+          const __nv_bfloat162 h2 = __floats2bfloat162_rn(__uint_as_float(v[2 * i]), __uint_as_float(v[2 * i + 1]));
+          v[i] = *reinterpret_cast<const uint32_t*>(&h2);
+        }
+#pragma unroll
+        for (int i = 0; i < kCols / 2; i += C::kYRow / 4) store(v + i, n0 + 2 * i);
+      } else {
+#pragma unroll
+        for (int i = 0; i < kCols; i += C::kYRow / 4) store(v + i, n0 + i);
+      }
     }
     if (lane == 0) bulk_wait_group0();  // output stores complete
-  } else if (warp == 14) {
+  } else if (warp == 2) {
     // ------------------------------------------------------ scale producer
     if (lane == 0) {
       uint32_t g = 0, issued = 0, issued_par = 0;
@@ -438,7 +417,8 @@ __global__ void __launch_bounds__(480, 1) gemm_fp4_kernel(const __grid_constant_
           if ((issued >> i) & 1u) (void)mbar_wait(&sfull[i], (issued_par >> i) & 1u, 1000000000ull, nullptr, true);
       }
     }
-  } else {
+  } else if (warp >= 4) {
+    regs_down<kFp4RegsLow>();
     // ------------------------------------------------ scale-slot staging
     const int q = warp & 3;
     const uint32_t tq = tmem_base + ((uint32_t)(32 * q) << 16);
@@ -449,24 +429,33 @@ __global__ void __launch_bounds__(480, 1) gemm_fp4_kernel(const __grid_constant_
       if (tile_expert((int64_t)xy.mt * C::BM * CTAS) < 0) continue;
       for (int kq = 0; kq < k_groups; kq++, g++) {
         const uint32_t ss = g % C::kSfStages, slot = g % C::kSlots;
+        bool ok = true;
         if (!mbar_wait(&sfull[ss], (g / C::kSfStages) & 1u, p.timeout_ns, abort_flag)) { give_up(); break; }
         const uint8_t* sb = sfbuf + ss * C::kSfBytes + 16 * lane;
-        uint4 x[C::kSfChunks], wv[C::kNRB * C::kSfChunks];
-#pragma unroll
-        for (int c = 0; c < C::kSfChunks; c++) {
-          x[c] = *reinterpret_cast<const uint4*>(sb + C::oSfx + 512 * c);
-#pragma unroll
-          for (int rb = 0; rb < C::kNRB; rb++)
-            wv[C::kNRB * c + rb] = *reinterpret_cast<const uint4*>(sb + C::oSfw + (rb * C::kSfChunks + c) * 512);
-        }
-        // the MMAs that used the slot before have retired
-        if (!mbar_wait(&slot_empty[slot], ((g / C::kSlots) & 1u) ^ 1u, p.timeout_ns, abort_flag)) { give_up(); break; }
-        tc_fence_after();
         const uint32_t st = tq + C::BN + slot * (uint32_t)C::kSlotCols;
+        constexpr int kPieces = (1 + C::kNRB) * C::kSfChunks;  // of 16 bytes a lane, in the slot's order of columns
+        auto piece = [&](int i) {
+          const int c = (i - C::kSfChunks) / C::kNRB, rb = (i - C::kSfChunks) % C::kNRB;
+          return *reinterpret_cast<const uint4*>(i < C::kSfChunks ? sb + C::oSfx + 512 * i
+                                                                  : sb + C::oSfw + (rb * C::kSfChunks + c) * 512);
+        };
 #pragma unroll
-        for (int c = 0; c < C::kSfChunks; c += 4) tmem_st16(st + C::cSfx + 4 * c, x + c);
+        for (int h = 0; h < 2; h++) {
+          uint4 v[kPieces / 2];
 #pragma unroll
-        for (int c = 0; c < C::kNRB * C::kSfChunks; c += 4) tmem_st16(st + C::cSfw + 4 * c, wv + c);
+          for (int i = 0; i < kPieces / 2; i++) v[i] = piece(h * (kPieces / 2) + i);
+          if (h == 0) {  // the MMAs that used the slot before have retired
+            ok = mbar_wait(&slot_empty[slot], ((g / C::kSlots) & 1u) ^ 1u, p.timeout_ns, abort_flag);
+            if (!ok) break;
+            tc_fence_after();
+          }
+          static_assert(kPieces % 4 == 0, "halves of stores of 16 and 8 columns");
+#pragma unroll
+          for (int i = 0; i + 4 <= kPieces / 2; i += 4) tmem_st16(st + 4 * (h * (kPieces / 2) + i), v + i);
+          if constexpr ((kPieces / 2) % 4 == 2)
+            tmem_st8(st + 4 * (h * (kPieces / 2) + kPieces / 2 - 2), v[kPieces / 2 - 2], v[kPieces / 2 - 1]);
+        }
+        if (!ok) { give_up(); break; }
         tmem_st_wait();
         tc_fence_before();
         __syncwarp();

@@ -830,6 +830,12 @@ sharq_status launch_gemm_fp4(const sharq_fp4* x, const sharq_fp4* w, const int32
   using C = Fp4Cfg<KIND, CTAS>;
   sharq_status st = ensure_smem_limit<gemm_fp4_kernel<KIND, CTAS>>(C::kSmemBytes);
   if (st != SHARQ_OK) return st;
+  // the kernel's warpgroups share out the registers that it is launched with
+  static const int regs = [] {
+    cudaFuncAttributes a;
+    return cudaFuncGetAttributes(&a, gemm_fp4_kernel<KIND, CTAS>) == cudaSuccess ? a.numRegs : 0;
+  }();
+  if (regs != kFp4GemmRegs) return fail(SHARQ_ERR_CUDA, "the FP4 GEMM was built for %d registers, not %d", regs, kFp4GemmRegs);
   const int64_t t = x->rows, n = w->rows, k = x->k, es = y_dt == SHARQ_BF16 ? 2 : 4;
   Fp4Maps maps;
   memset(&maps, 0, sizeof(maps));
@@ -855,7 +861,7 @@ sharq_status launch_gemm_fp4(const sharq_fp4* x, const sharq_fp4* w, const int32
   const int64_t tiles = ((t + C::BM * CTAS - 1) / (C::BM * CTAS)) * ((n + C::BN - 1) / C::BN);
   if (tiles > INT32_MAX / 2) return fail(SHARQ_ERR_UNSUPPORTED, "%lld output tiles", (long long)tiles);
   const int64_t slots = sm_count() / CTAS;
-  return launch_ex(gemm_fp4_kernel<KIND, CTAS>, dim3((unsigned)(CTAS * (tiles < slots ? tiles : slots))), dim3(480),
+  return launch_ex(gemm_fp4_kernel<KIND, CTAS>, dim3((unsigned)(CTAS * (tiles < slots ? tiles : slots))), dim3(kFp4GemmThreads),
                    C::kSmemBytes, s, CTAS, maps, gp);
 }
 
