@@ -23,21 +23,21 @@ struct Fp4Cfg {
   static constexpr int kWBytes = BNh * 128, kXBytes = BM * 128;
   // a ring of operand stages of BK each
   static constexpr int oW = 0, oX = oW + kWBytes, kStageBytes = oX + kXBytes;
-  static constexpr int kStages = CTAS == 2 ? 5 : 4;
+  static constexpr int kStages = CTAS == 2 ? 5 : 3;
   // The scales go a step further, shared -> tensor memory, by warps whose waits
   // and barriers cost more than the copy: they move two K tiles' worth at a
   // time, in rings of their own in both memories.
   static constexpr int kSfTiles = 2, kSfChunks = kSfTiles * kChunks;
   static constexpr int kSfx = kSfChunks * 512, kSfw = kNRB * kSfChunks * 512;
   static constexpr int oSfx = 0, oSfw = oSfx + kSfx, kSfBytes = oSfw + kSfw;
-  static constexpr int kSfStages = CTAS == 2 ? 3 : 2;
+  static constexpr int kSfStages = 2;
   // tensor memory: accumulator, then the scale slots
   static constexpr int cSfx = 0, cSfw = 4 * kSfChunks, kSlotCols = 4 * (1 + kNRB) * kSfChunks;
   static constexpr int kSlots = 2;
   static_assert(kNRB == 2, "256 weight rows");
   static constexpr int kTmemCols = 512;
   static_assert(BN + kSlots * kSlotCols <= kTmemCols, "tensor memory budget");
-  static constexpr int kYRow = CTAS == 2 ? 64 : 16;   // bytes of an output row staged at a time, per warp
+  static constexpr int kYRow = 128;             // bytes of an output row staged at a time, per epilogue warp
   static constexpr int kYBuf = 8 * 32 * kYRow;
   static constexpr int kSmemBytes = kStages * kStageBytes + kSfStages * kSfBytes + kYBuf + 8 * 128 * 4 + 1024 /*align*/ + 256 /*barriers*/;
   static_assert(kSmemBytes <= 232448, "shared memory budget");
@@ -329,14 +329,16 @@ __global__ void __launch_bounds__(kFp4GemmThreads, 1) gemm_fp4_kernel(const __gr
       it++;
       tc_fence_after();
       const int32_t row0 = (int32_t)(row - lane);
-      // kYRow bytes of each row at a time through shared memory, written by TMA
-      // stores (whole lines; rows at or beyond t and columns from n on are clipped)
-      auto store = [&](const uint32_t* w, int64_t col) {  // kYRow / 4 words of each lane's row
+      // 128 bytes of each row at a time through shared memory (in the tensor map's
+      // 128-byte swizzle, so that neither side meets bank conflicts), written by a
+      // TMA store: whole lines; rows at or beyond t and columns from n on are clipped
+      auto store = [&](const uint32_t* w, int64_t col) {
         if (lane == 0) bulk_wait_group_read0();  // the previous store has read the buffer
         __syncwarp();
-        uint4* d = reinterpret_cast<uint4*>(yb + C::kYRow * lane);
 #pragma unroll
-        for (int j = 0; j < C::kYRow / 16; j++) d[j] = make_uint4(w[4 * j], w[4 * j + 1], w[4 * j + 2], w[4 * j + 3]);
+        for (int j = 0; j < 8; j++)
+          *reinterpret_cast<uint4*>(yb + C::kYRow * lane + ((j ^ (lane & 7)) << 4)) =
+              make_uint4(w[4 * j], w[4 * j + 1], w[4 * j + 2], w[4 * j + 3]);
         fence_proxy_async_smem();
         __syncwarp();
         if (lane == 0 && col < p.n) {

@@ -843,7 +843,7 @@ sharq_status launch_gemm_fp4(const sharq_fp4* x, const sharq_fp4* w, const int32
   if (st != SHARQ_OK) return st;
   st = make_map(&maps.w, w->codes, k / 2, n * w->experts, 128, C::BNh, CU_TENSOR_MAP_SWIZZLE_128B);
   if (st != SHARQ_OK) return st;
-  st = make_map(&maps.y, y, n * es, t, C::kYRow, 32, CU_TENSOR_MAP_SWIZZLE_NONE);
+  st = make_map(&maps.y, y, n * es, t, C::kYRow, 32, CU_TENSOR_MAP_SWIZZLE_128B);
   if (st != SHARQ_OK) return st;
   Fp4GemmParams gp;
   memset(&gp, 0, sizeof(gp));
