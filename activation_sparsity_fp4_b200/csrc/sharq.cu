@@ -16,6 +16,7 @@
 #include "fp4.cuh"
 #include "gemm.cuh"
 #include "gemm_fp4.cuh"
+#include "gemm_fp4_few.cuh"
 #include "gemm_pair.cuh"
 #include "gemm_swap.cuh"
 #include "gemv.cuh"
@@ -865,6 +866,73 @@ sharq_status launch_gemm_fp4(const sharq_fp4* x, const sharq_fp4* w, const int32
                    C::kSmemBytes, s, CTAS, maps, gp);
 }
 
+// Few rows: weight tiles of 128 rows, the K loop of each split over a cluster.
+template <int KIND, int TN>
+sharq_status launch_fp4_few(const sharq_fp4* x, const sharq_fp4* w, void* y, sharq_dtype y_dt, cudaStream_t s) {
+  using C = Fp4FewCfg<KIND, TN>;
+  sharq_status st = ensure_smem_limit<gemm_fp4_few_kernel<KIND, TN>>(C::kSmemBytes);
+  if (st != SHARQ_OK) return st;
+  const int64_t t = x->rows, n = w->rows, k = x->k;
+  Fp4FewMaps maps;
+  memset(&maps, 0, sizeof(maps));
+  st = make_map(&maps.w, w->codes, k / 2, n, 128, C::BM, CU_TENSOR_MAP_SWIZZLE_128B);
+  if (st != SHARQ_OK) return st;
+  st = make_map(&maps.x, x->codes, k / 2, t, 128, TN, CU_TENSOR_MAP_SWIZZLE_128B);
+  if (st != SHARQ_OK) return st;
+  Fp4FewParams fp;
+  memset(&fp, 0, sizeof(fp));
+  fp.t = t;
+  fp.n = n;
+  fp.k = k;
+  fp.sf_w = static_cast<const uint8_t*>(w->scales);
+  fp.sf_x = static_cast<const uint8_t*>(x->scales);
+  fp.row_w = w->row_scale;
+  fp.row_x = x->row_scale;
+  fp.y = y;
+  fp.y_bf16 = y_dt == SHARQ_BF16;
+  fp.timeout_ns = wait_timeout_ns();
+  const int64_t tiles = ((n + C::BM - 1) / C::BM) * ((t + TN - 1) / TN), k_tiles = (k + C::BK - 1) / C::BK;
+  // slices: enough CTAs for every SM, two K tiles each at least, at most 8 (the
+  // portable cluster size), and no more than let all clusters be resident at once
+  int64_t split = sm_count() / tiles;
+  if (split > k_tiles / 2) split = k_tiles / 2;
+  if (split > kFp4FewMaxSplit) split = kFp4FewMaxSplit;
+  static std::atomic<int> resident[kFp4FewMaxSplit + 1];  // clusters of each size, + 1
+  auto fits = [&](int64_t cs) {
+    int r = resident[cs].load(std::memory_order_relaxed);
+    if (r == 0) {
+      r = 1 + max_active_clusters(gemm_fp4_few_kernel<KIND, TN>, 192, C::kSmemBytes, (int)cs);
+      resident[cs].store(r, std::memory_order_relaxed);
+    }
+    return r - 1 >= tiles;
+  };
+  while (split > 1 && !fits(split)) split--;
+  if (split < 1) split = 1;
+  fp.split = (int32_t)split;
+  if (tiles * split > INT32_MAX) return fail(SHARQ_ERR_UNSUPPORTED, "%lld output tiles", (long long)tiles);
+  return launch_ex(gemm_fp4_few_kernel<KIND, TN>, dim3((unsigned)(tiles * split)), dim3(192), C::kSmemBytes, s,
+                   (unsigned)split, maps, fp);
+}
+template <int KIND>
+sharq_status fp4_few(const sharq_fp4* x, const sharq_fp4* w, void* y, sharq_dtype y_dt, cudaStream_t s) {
+  if (x->rows <= 32) return launch_fp4_few<KIND, 32>(x, w, y, y_dt, s);
+  if (x->rows <= 64) return launch_fp4_few<KIND, 64>(x, w, y, y_dt, s);
+  return launch_fp4_few<KIND, 128>(x, w, y, y_dt, s);
+}
+// The few-row kernel serves one round of its tiles on the SMs, for up to 64 rows,
+// or where every tile can be cut in slices of at least four K tiles.  NVFP4, us,
+// few-row kernel against CTA pairs: 1 x 4096 x 14336 9.3 / 23.6, 64 x 4096 x 4096
+// 7.2 / 10.8, 256 x 4096 x 4096 11.2 / 11.4, 1000 x 512 x 14336 12.5 / 24.5; on
+// the other side 128 x 16384 x 4096 15.0 / 12.7, 512 x 4096 x 14336 31.3 / 25.5,
+// 1000 x 1024 x 1024 8.6 / 7.1, 32 x 32768 x 4096 22.6 / 20.2.
+bool fp4_few_rows(int64_t t, int64_t n, int64_t k) {
+  const int64_t tn = t <= 32 ? 32 : t <= 64 ? 64 : 128;
+  const int64_t tiles = ((n + 127) / 128) * ((t + tn - 1) / tn), k_tiles = (k + 255) / 256, sms = sm_count();
+  if (tiles > sms) return false;
+  const int64_t split = sms / tiles < kFp4FewMaxSplit ? sms / tiles : kFp4FewMaxSplit;
+  return t <= 64 || (split >= 2 && k_tiles >= 8);
+}
+
 sharq_status run_linear_fp4(const sharq_fp4* x, const sharq_fp4* w, const int32_t* offsets, void* y, sharq_dtype y_dt,
                             cudaStream_t s) {
   sharq_status st = check_fp4(x, "activations");
@@ -884,6 +952,8 @@ sharq_status run_linear_fp4(const sharq_fp4* x, const sharq_fp4* w, const int32_
   if (offsets)
     return x->fmt == SHARQ_NVFP4 ? launch_gemm_fp4<GK_NVF4, 1>(x, w, offsets, y, y_dt, s)
                                  : launch_gemm_fp4<GK_MXF4, 1>(x, w, offsets, y, y_dt, s);
+  if (fp4_few_rows(x->rows, w->rows, x->k))
+    return x->fmt == SHARQ_NVFP4 ? fp4_few<GK_NVF4>(x, w, y, y_dt, s) : fp4_few<GK_MXF4>(x, w, y, y_dt, s);
   return x->fmt == SHARQ_NVFP4 ? launch_gemm_fp4<GK_NVF4, 2>(x, w, nullptr, y, y_dt, s)
                                : launch_gemm_fp4<GK_MXF4, 2>(x, w, nullptr, y, y_dt, s);
 }
