@@ -20,6 +20,9 @@ struct RouteParams {
   float scale;
   int32_t* ids;
   float* weights;
+  int32_t smem_doubles;     // shared memory of a warp (grouped form)
+  int32_t lanes_per_group;  // a power of two
+  uint32_t per_magic;       // ceil(2^32 / (experts / groups)): e / per = umulhi(e, per_magic) for e <= 512; 0: per = 1
 };
 
 __device__ __forceinline__ double warp_max(double v) {
@@ -33,16 +36,11 @@ __device__ __forceinline__ double warp_sum(double v) {
   return v;
 }
 
-// One warp per token; lane l holds the experts l, l + 32, ... (VPL of them).
+// Scores, selection and weights of one token in 64 bits, by one warp; lane l holds the experts l, l + 32, ....
 template <int VPL, bool XBF16>
-__global__ void __launch_bounds__(128) route_kernel(const RouteParams p) {
-  extern __shared__ double route_smem[];  // per warp: the experts' selection scores (grouped form)
-  const int lane = threadIdx.x & 31, w = threadIdx.x >> 5;
+__device__ __noinline__ void route_exact(const RouteParams& p, int64_t tok, double* sc /* experts, grouped form */) {
+  const int lane = threadIdx.x & 31;
   const double ninf = -__longlong_as_double(0x7FF0000000000000ll);
-  grid_dep_wait();
-  grid_dep_launch();
-  const int64_t tok = (int64_t)blockIdx.x * 4 + w;
-  if (tok >= p.t) return;
   float l[VPL];
   double s[VPL], c[VPL];  // score p, selection value
   double m = ninf;
@@ -82,32 +80,32 @@ __global__ void __launch_bounds__(128) route_kernel(const RouteParams p) {
     c[i] = l[i] > -INFINITY && v > ninf ? v : ninf;
   }
   if (p.groups > 1) {
-    double* sc = route_smem + w * p.experts;
     const int per = p.experts / p.groups;
 #pragma unroll
     for (int i = 0; i < VPL; i++)
       if (lane + 32 * i < p.experts) sc[lane + 32 * i] = c[i];
     __syncwarp();
-    double gv = ninf;
-    if (lane < p.groups) {
-      double a = ninf, b = ninf;
-      for (int j = 0; j < per; j++) {
-        const double v = sc[lane * per + j];
-        if (v > a) {
-          b = a;
-          a = v;
-        } else if (v > b) {
-          b = v;
-        }
+    const int lpg = p.lanes_per_group, g = lane / lpg, sub = lane & (lpg - 1);
+    double a = ninf, b = ninf;  // the group's two largest
+    if (g < p.groups)
+      for (int j = sub; j < per; j += lpg) {
+        const double v = sc[g * per + j];
+        b = fmax(b, fmin(a, v));
+        a = fmax(a, v);
       }
-      gv = p.group_top == 2 && b > ninf ? a + b : a;
+    for (int d = 1; d < lpg; d <<= 1) {
+      const double oa = __shfl_xor_sync(0xffffffffu, a, d), ob = __shfl_xor_sync(0xffffffffu, b, d);
+      b = fmax(fmin(a, oa), fmax(b, ob));
+      a = fmax(a, oa);
     }
+    const double gv = p.group_top == 2 && b > ninf ? a + b : a;
     int before = 0;  // groups that come before this lane's
-    for (int g = 0; g < p.groups; g++) {
-      const double o = __shfl_sync(0xffffffffu, gv, g);
-      before += o > gv || (o == gv && g < lane);
+    for (int o = 0; o < p.groups; o++) {
+      const double ov = __shfl_sync(0xffffffffu, gv, o * lpg);
+      before += ov > gv || (ov == gv && o < g);
     }
-    const uint32_t kept = __ballot_sync(0xffffffffu, lane < p.groups && before < p.top_groups);
+    const uint32_t kept =
+        __reduce_or_sync(0xffffffffu, g < p.groups && sub == 0 && before < p.top_groups ? 1u << g : 0u);
 #pragma unroll
     for (int i = 0; i < VPL; i++) {
       const int e = lane + 32 * i;
@@ -119,35 +117,39 @@ __global__ void __launch_bounds__(128) route_kernel(const RouteParams p) {
     for (int i = 0; i < VPL; i++)
       if (c[i] > ninf) c[i] = (double)l[i];
   }
+  // ordered bits of the values, 0 for none
+  uint64_t key[VPL];
+#pragma unroll
+  for (int i = 0; i < VPL; i++) {
+    const uint64_t u = (uint64_t)__double_as_longlong(c[i] + 0.0);
+    key[i] = c[i] > ninf ? u ^ ((u >> 63) ? ~0ull : 1ull << 63) : 0;
+  }
   double sum = 0.0, mine = 0.0;
   int my_id = -1;
   for (int j = 0; j < p.top_k; j++) {
-    double best = ninf, bs = 0.0;
-    int be = 0x7FFFFFFF;
+    uint64_t best = 0;
+#pragma unroll
+    for (int i = 0; i < VPL; i++) best = key[i] > best ? key[i] : best;
+    const uint32_t hi = __reduce_max_sync(0xffffffffu, (uint32_t)(best >> 32));
+    const uint32_t lo = __reduce_max_sync(0xffffffffu, (uint32_t)(best >> 32) == hi ? (uint32_t)best : 0u);
+    const uint64_t top = (uint64_t)hi << 32 | lo;
+    if (top == 0) break;  // no eligible expert left (the same in every lane)
+    uint32_t e = 0xFFFFFFFFu;
+#pragma unroll
+    for (int i = VPL - 1; i >= 0; i--)
+      if (key[i] == top) e = (uint32_t)(lane + 32 * i);
+    e = __reduce_min_sync(0xffffffffu, e);
+    double bs = 0.0;
 #pragma unroll
     for (int i = 0; i < VPL; i++)
-      if (c[i] > best) {
-        best = c[i];
+      if ((uint32_t)(lane + 32 * i) == e) {
+        key[i] = 0;
         bs = s[i];
-        be = lane + 32 * i;
       }
-#pragma unroll
-    for (int msk = 16; msk >= 1; msk >>= 1) {
-      const double ob = __shfl_xor_sync(0xffffffffu, best, msk), os = __shfl_xor_sync(0xffffffffu, bs, msk);
-      const int oe = __shfl_xor_sync(0xffffffffu, be, msk);
-      if (ob > best || (ob == best && oe < be)) {
-        best = ob;
-        bs = os;
-        be = oe;
-      }
-    }
-    if (be == 0x7FFFFFFF) break;  // no eligible expert left (the same in every lane)
-#pragma unroll
-    for (int i = 0; i < VPL; i++)
-      if (lane + 32 * i == be) c[i] = ninf;
+    bs = __shfl_sync(0xffffffffu, bs, (int)(e & 31u));
     sum += bs;
     if (lane == j) {
-      my_id = be;
+      my_id = (int)e;
       mine = bs;
     }
   }
@@ -159,11 +161,257 @@ __global__ void __launch_bounds__(128) route_kernel(const RouteParams p) {
   }
 }
 
+// Order-preserving bits of a float (0 stands for "not eligible": no value but a NaN maps to it).
+__device__ __forceinline__ uint32_t ordered_bits(float v) {
+  const uint32_t b = __float_as_uint(v + 0.0f);  // -0 and 0 are one value
+  return b ^ ((b >> 31) ? 0xFFFFFFFFu : 0x80000000u);
+}
+__device__ __forceinline__ float from_ordered_bits(uint32_t u) {
+  return __uint_as_float(u ^ ((u >> 31) ? 0x80000000u : 0xFFFFFFFFu));
+}
+
+// Sorts N values (a power of two) in descending order by Batcher's odd-even merges.
+template <int N>
+__device__ __forceinline__ void sort_desc(uint32_t (&v)[N]) {
+#pragma unroll
+  for (int p = 1; p < N; p *= 2)
+#pragma unroll
+    for (int k = p; k >= 1; k /= 2)
+#pragma unroll
+      for (int j = k % p; j + k < N; j += 2 * k)
+#pragma unroll
+        for (int i = 0; i < k; i++)
+          if (i + j + k < N && (i + j) / (2 * p) == (i + j + k) / (2 * p)) {
+            const uint32_t a = v[i + j], b = v[i + j + k];
+            v[i + j] = a > b ? a : b;
+            v[i + j + k] = a > b ? b : a;
+          }
+}
+
+// One warp per token.  Scores are formed in fp32, ranked by redux.sync on their
+// ordered bits, and the ranking is taken where it is certain: neighbours that
+// decide (the top_k and the one after, the groups on either side of the border)
+// further apart than fp32's error, or equal in all that makes them.  A token where they
+// are not is ranked again in 64 bits.  Without a bias the logits themselves are
+// ranked, which is exact.  Error of a score made for ranking: __expf(x) is within
+// 2 + 1.2 |x| units of 2^-23; of that e^x a sigmoid 1 / (1 + e^-l) = s passes on the
+// part 1 - s and adds 1 + 4 units of 2^-24; the softmax adds at most 16 + 5 for its
+// sum, what the sum's own exponentials are off by (their mean, under 2^-20) and 3
+// more, 2^-19 in all; the bias 2^-24 of c.  The weights are made with expf.
+// 16384 tokens x 256 experts, 8 groups, bias: all in 64 bits took 55 us.
+template <int VPL, bool XBF16>
+__global__ void __launch_bounds__(128, VPL == 16 ? 5 : 10) route_kernel(const RouteParams p) {
+  extern __shared__ double route_smem[];  // per warp: the experts' selection values (grouped form)
+  const int lane = threadIdx.x & 31, w = threadIdx.x >> 5;
+  grid_dep_wait();
+  grid_dep_launch();
+  const int64_t tok = (int64_t)blockIdx.x * 4 + w;
+  if (tok >= p.t) return;
+  const int64_t row = tok * p.stride;
+  auto logit = [&](int e) {
+    if constexpr (XBF16) return __bfloat162float(static_cast<const __nv_bfloat16*>(p.logits)[row + e]);
+    else return static_cast<const float*>(p.logits)[row + e];
+  };
+  const bool scores = p.bias != nullptr || p.groups > 1;  // whether the scores take part in the selection
+  float l[VPL], c[VPL];
+  float m = -INFINITY;
+#pragma unroll
+  for (int i = 0; i < VPL; i++) {
+    const int e = lane + 32 * i;
+    l[i] = e < p.experts ? logit(e) : -INFINITY;
+    m = fmaxf(m, l[i]);  // a NaN is passed over
+  }
+  float sum = 1.0f;
+  if (p.softmax) {
+    m = from_ordered_bits(__reduce_max_sync(0xffffffffu, ordered_bits(m)));
+    if (scores || !p.renormalize) {
+      sum = 0.0f;
+#pragma unroll
+      for (int i = 0; i < VPL; i++) {
+        c[i] = l[i] == m ? 1.0f : (l[i] > -INFINITY ? __expf(l[i] - m) : 0.0f);
+        sum += c[i];
+      }
+#pragma unroll
+      for (int msk = 16; msk >= 1; msk >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, msk);
+    }
+  }
+  const float scale_p = p.softmax ? 1.0f / sum : 1.0f;
+  auto score = [&](float v) -> float {
+    if (p.softmax) return (v == m ? 1.0f : expf(v - m)) * scale_p;
+    return 1.0f / (1.0f + expf(-v));
+  };
+  // no score, fast or not, is further off than this: s (1 - s) (2 + 1.2 |l|) < 0.56 and e^x (2 + 1.2 |x|) <= 2
+  const float off = p.softmax ? scale_p * (0x1p-22f + 0x1p-19f) : 0.56f * 0x1p-23f + 0x1p-21f;
+  uint32_t key[VPL];
+  bool unsure = false;
+#pragma unroll
+  for (int i = 0; i < VPL; i++) key[i] = l[i] > -INFINITY ? ordered_bits(l[i]) : 0u;
+  if (scores) {
+    uint32_t kept = 0xFFFFFFFFu;
+#pragma unroll
+    for (int i = 0; i < VPL; i++) {
+      const int e = lane + 32 * i;
+      const float s = p.softmax ? c[i] * scale_p : __fdividef(1.0f, 1.0f + __expf(-l[i]));
+      c[i] = key[i] ? s + (p.bias ? __ldg(p.bias + e) : 0.0f) : -INFINITY;
+      if (!(c[i] > -INFINITY)) {
+        c[i] = -INFINITY;
+        key[i] = 0;
+      }
+    }
+    if (p.groups > 1) {
+      // lanes [g lpg, (g + 1) lpg) find group g's two largest; lpg floats between
+      // the groups in shared memory keep their reads on different banks
+      const int lpg = p.lanes_per_group, per = p.experts / p.groups, g = lane / lpg, sub = lane & (lpg - 1);
+      // one expert a group and no bias: the groups' best logits rank them as their scores do
+      const bool by_logit = p.group_top == 1 && !p.bias;
+      float* sc = reinterpret_cast<float*>(route_smem + (size_t)w * p.smem_doubles);
+      auto group_of = [&](int e) { return p.per_magic ? (int)__umulhi((uint32_t)e, p.per_magic) : e; };
+#pragma unroll
+      for (int i = 0; i < VPL; i++) {
+        const int e = lane + 32 * i;
+        if (e < p.experts) sc[e + lpg * group_of(e)] = by_logit ? (key[i] ? l[i] : -INFINITY) : c[i];
+      }
+      __syncwarp();
+      float a = -INFINITY, b = -INFINITY;
+      if (g < p.groups) {
+        const float* sg = sc + g * (per + lpg);
+        for (int j = sub; j < per; j += lpg) {
+          const float v = sg[j];
+          b = fmaxf(b, fminf(a, v));
+          a = fmaxf(a, v);
+        }
+      }
+      for (int d = 1; d < lpg; d <<= 1) {
+        const float oa = __shfl_xor_sync(0xffffffffu, a, d), ob = __shfl_xor_sync(0xffffffffu, b, d);
+        b = fmaxf(fminf(a, oa), fmaxf(b, ob));
+        a = fmaxf(a, oa);
+      }
+      const float gv = p.group_top == 2 && b > -INFINITY ? a + b : a;
+      int before = 0;  // groups ahead of this lane's
+      for (int o = 0; o < p.groups; o++) {
+        const float ov = __shfl_sync(0xffffffffu, gv, o * lpg);
+        before += ov > gv || (ov == gv && o < g);
+      }
+      // the border: the last group inside and the first outside
+      const bool head = g < p.groups && sub == 0;
+      const float in = from_ordered_bits(__reduce_min_sync(
+          0xffffffffu, head && before < p.top_groups ? ordered_bits(gv) : 0xFFFFFFFFu));
+      const float out = from_ordered_bits(__reduce_max_sync(
+          0xffffffffu, head && before >= p.top_groups ? ordered_bits(gv) : 0u));
+      if (p.top_groups < p.groups && out > -INFINITY && in < INFINITY) {
+        if (by_logit)  // except where even 64 bits may round the scores of different logits to one value
+          unsure = in != out && (in - out < 0x1p-24f || (p.softmax ? m - in > 700.0f : in > 15.0f || in < -700.0f));
+        else  // two scores on each side; without a bias they are the whole value: off by 110 of 2^-23 of it (|x| to 88)
+          unsure = in - out <= (p.bias ? 4.0f * off : fminf(4.0f * off, 0x1p-14f * in)) + 0x1p-21f * fabsf(in) + 0x1p-120f;
+      }
+      uint32_t mine = head && before < p.top_groups ? 1u << g : 0u;
+      kept = __reduce_or_sync(0xffffffffu, mine);
+#pragma unroll
+      for (int i = 0; i < VPL; i++)
+        if (!((kept >> (group_of(lane + 32 * i) & 31)) & 1u)) key[i] = 0;
+    }
+    if (p.bias) {
+#pragma unroll
+      for (int i = 0; i < VPL; i++)
+        if (key[i]) key[i] = ordered_bits(c[i]);
+    }
+  }
+  // The top_k keys in order, and with a bias the one after them.  First on words
+  // of the key's upper 23 bits and the expert (lower experts larger): all words
+  // differ, each lane keeps its own sorted, and a round takes the largest head.
+  int my_id = -1;
+  int after_id = -1;  // lane top_k - 1: the one after
+  const int rounds = p.top_k + 1;
+  uint32_t last = 0, mine = 0;  // the last word taken; lane j's, of round j
+  bool close = false;           // neighbours that the upper bits do not tell apart
+  {
+    uint32_t word[VPL];
+#pragma unroll
+    for (int i = 0; i < VPL; i++)
+      word[i] = key[i] ? (key[i] & 0xFFFFFE00u) | (511u - (uint32_t)(lane + 32 * i)) : 0u;
+    sort_desc<VPL>(word);
+    for (int j = 0; j < rounds; j++) {
+      const uint32_t top = __reduce_max_sync(0xffffffffu, word[0]);
+      if (top == 0) break;
+      if (word[0] == top) {
+#pragma unroll
+        for (int i = 0; i + 1 < VPL; i++) word[i] = word[i + 1];
+        word[VPL - 1] = 0;
+      }
+      // bf16 logits have 16 bits: equal here is equal, and the lower expert is first
+      if ((!XBF16 || p.bias) && j > 0 && ((last ^ top) >> 9) == 0) close = true;
+      last = top;
+      if (lane == j) mine = top;
+    }
+    const uint32_t next = p.top_k < 32 ? __shfl_sync(0xffffffffu, mine, p.top_k & 31) : last;
+    if (lane < p.top_k && mine) my_id = 511 - (int)(mine & 511u);
+    // with all 32 places taken the last word is the one after only if it was not the last place's own
+    if (next && next != __shfl_sync(0xffffffffu, mine, p.top_k - 1)) after_id = 511 - (int)(next & 511u);
+  }
+  if (close) {  // the same on whole keys
+    my_id = after_id = -1;
+    for (int j = 0; j < rounds; j++) {
+      uint32_t best = 0;
+#pragma unroll
+      for (int i = 0; i < VPL; i++) best = key[i] > best ? key[i] : best;
+      const uint32_t top = __reduce_max_sync(0xffffffffu, best);
+      if (top == 0) break;
+      uint32_t e = 0xFFFFFFFFu;
+#pragma unroll
+      for (int i = VPL - 1; i >= 0; i--)
+        if (key[i] == top) e = (uint32_t)(lane + 32 * i);
+      e = __reduce_min_sync(0xffffffffu, e);
+#pragma unroll
+      for (int i = 0; i < VPL; i++)
+        if ((uint32_t)(lane + 32 * i) == e) key[i] = 0;
+      if (j == p.top_k) after_id = (int)e;
+      else if (lane == j) my_id = (int)e;
+    }
+  }
+  const float ml = my_id >= 0 ? logit(my_id) : -INFINITY;
+  float wv = my_id >= 0 ? score(ml) : 0.0f;
+  if (p.bias) {
+    // every place against the next one
+    // (the ranking's scores and these, of either place, and the ranking's of an expert behind: four errors)
+    const float mb = my_id >= 0 ? __ldg(p.bias + my_id) : 0.0f, mc = wv + mb;
+    float nl = __shfl_down_sync(0xffffffffu, ml, 1), nb = __shfl_down_sync(0xffffffffu, mb, 1);
+    float nw = __shfl_down_sync(0xffffffffu, wv, 1);
+    int ni = __shfl_down_sync(0xffffffffu, my_id, 1);
+    if (lane == p.top_k - 1) {
+      ni = after_id;
+      if (ni >= 0) {
+        nl = logit(ni);
+        nb = __ldg(p.bias + ni);
+        nw = score(nl);
+      }
+    }
+    if (my_id >= 0 && ni >= 0 && lane < p.top_k) {
+      const bool same = ml == nl && mb == nb;
+      if (!same && mc - (nw + nb) <= 4.0f * off + 0x1p-22f * fabsf(mc) && mc < INFINITY) unsure = true;
+    }
+  }
+  float total = wv;
+  if (p.renormalize) {
+#pragma unroll
+    for (int msk = 16; msk >= 1; msk >>= 1) total += __shfl_xor_sync(0xffffffffu, total, msk);
+    // so small a sum has lost bits to underflow
+    if (total < 0x1p-90f && __any_sync(0xffffffffu, my_id >= 0)) unsure = true;
+  }
+  if (__any_sync(0xffffffffu, unsure)) {
+    route_exact<VPL, XBF16>(p, tok, route_smem + (size_t)w * p.smem_doubles);
+    return;
+  }
+  if (lane < p.top_k) {
+    if (p.renormalize) wv = my_id >= 0 ? wv / total : 0.0f;
+    p.ids[tok * p.top_k + lane] = my_id;
+    p.weights[tok * p.top_k + lane] = wv * p.scale;
+  }
+}
+
 // ------------------------------------------------------------ row layout
 // A stable counting sort by one cluster of CTAs: each CTA takes a contiguous
 // share of the ids, each warp a contiguous share of that.  Pass 1 counts every
-// warp's ids per expert (a warp's equal ids found by match, so no atomics and
-// one order only); the counts are prefixed over the warps of a CTA, then over
+// warp's ids per expert; the counts are prefixed over the warps of a CTA, then over
 // the cluster's CTAs through distributed shared memory, and the experts'
 // padded sizes give the offsets.  Pass 2 walks the same ids again and hands
 // out the rows.
@@ -178,47 +426,69 @@ struct RowsParams {
 };
 constexpr int kRowsWarps = 32;
 
+constexpr int kRowsBits = 10;  // an expert below kMaxExperts, or -1
+static_assert(kMaxExperts <= 1 << (kRowsBits - 1), "the last bit tells -1 apart");
+constexpr int kRowsBatch = 8;  // steps of a warp whose ids are loaded together
+
 __global__ void __launch_bounds__(kRowsWarps * 32) route_rows_kernel(const RowsParams p) {
   extern __shared__ int32_t rows_smem[];
   const int E = p.experts;
-  int32_t* hist = rows_smem;                // [warp][E]
-  int32_t* total = hist + kRowsWarps * E;   // this CTA's ids per expert
-  int32_t* count = total + E;               // the cluster's
-  int32_t* off = count + E;                 // E + 1 padded offsets
+  int32_t* hist = rows_smem;               // [warp][E]
+  int32_t* total = hist + kRowsWarps * E;  // this CTA's ids per expert
+  int32_t* count = total + E;              // the cluster's
+  int32_t* base = count + E;               // first row of this CTA's
+  int32_t* off = base + E;                 // E + 1 padded offsets
   __shared__ int32_t wsum[kRowsWarps];
   const int lane = threadIdx.x & 31, w = threadIdx.x >> 5;
   const int ctas = (int)gridDim.x, rank = (int)blockIdx.x;  // one cluster
+  int32_t* hw = hist + w * E;
+  for (int e = lane; e < E; e += 32) hw[e] = 0;
   grid_dep_wait();
   grid_dep_launch();
   const int64_t parts = (int64_t)ctas * kRowsWarps, part = (int64_t)rank * kRowsWarps + w;
-  const int64_t lo = p.n * part / parts, hi = p.n * (part + 1) / parts;
-  int32_t* hw = hist + w * E;
-  for (int e = lane; e < E; e += 32) hw[e] = 0;
+  // shares in whole steps of 32 ids
+  const int64_t steps = (p.n + 31) / 32, lo = steps * part / parts * 32, hi_ = steps * (part + 1) / parts * 32;
+  const int64_t hi = hi_ < p.n ? hi_ : p.n;
+  // the ids of kRowsBatch steps from i0 on: -1 for none
+  auto load = [&](int64_t i0, int (&e)[kRowsBatch]) {
+#pragma unroll
+    for (int b = 0; b < kRowsBatch; b++) {
+      const int64_t i = i0 + 32 * b + lane;
+      e[b] = i < hi ? __ldg(p.ids + i) : -1;
+    }
+#pragma unroll
+    for (int b = 0; b < kRowsBatch; b++)
+      if (e[b] < 0 || e[b] >= E) e[b] = -1;
+  };
   __syncwarp();
-  for (int64_t i0 = lo; i0 < hi; i0 += 32) {
-    const int64_t i = i0 + lane;
-    int e = i < hi ? p.ids[i] : -1;
-    if (e < 0 || e >= E) e = -1;
-    const uint32_t same = __match_any_sync(0xffffffffu, e);
-    if (e >= 0 && lane == __ffs(same) - 1) hw[e] += __popc(same);
-    __syncwarp();
+  for (int64_t i0 = lo; i0 < hi; i0 += 32 * kRowsBatch) {
+    int ids[kRowsBatch];
+    load(i0, ids);
+#pragma unroll
+    for (int b = 0; b < kRowsBatch; b++)
+      if (ids[b] >= 0) atomicAdd(hw + ids[b], 1);  // counts alone: their order changes nothing
   }
   __syncthreads();
   for (int e = threadIdx.x; e < E; e += blockDim.x) {  // exclusive prefix over the warps
     int run = 0;
-    for (int q = 0; q < kRowsWarps; q++) {
-      const int v = hist[q * E + e];
-      hist[q * E + e] = run;
-      run += v;
+    for (int q0 = 0; q0 < kRowsWarps; q0 += 8) {
+      int v[8];
+#pragma unroll
+      for (int q = 0; q < 8; q++) v[q] = hist[(q0 + q) * E + e];
+#pragma unroll
+      for (int q = 0; q < 8; q++) {
+        hist[(q0 + q) * E + e] = run;
+        run += v[q];
+      }
     }
     total[e] = run;
   }
   __syncthreads();
   cluster_sync_all();
-  int padded = 0;
+  int padded = 0, before = 0;
   if (threadIdx.x < (unsigned)E) {  // E <= 512 threads
     const int e = threadIdx.x;
-    int all = 0, before = 0;
+    int all = 0;
     for (int r = 0; r < ctas; r++) {
       int v;
       asm volatile("ld.shared::cluster.s32 %0, [%1];" : "=r"(v) : "r"(mapa_u32(smem_u32(total + e), (uint32_t)r)) : "memory");
@@ -227,8 +497,6 @@ __global__ void __launch_bounds__(kRowsWarps * 32) route_rows_kernel(const RowsP
     }
     count[e] = all;
     padded = (all + 127) / 128 * 128;
-    hist[e] += before;  // warp 0's prefix; the other warps' below
-    for (int q = 1; q < kRowsWarps; q++) hist[q * E + e] += before;
   }
   // inclusive scan of the padded sizes over the block
   int run = padded;
@@ -239,27 +507,44 @@ __global__ void __launch_bounds__(kRowsWarps * 32) route_rows_kernel(const RowsP
   }
   if (lane == 31) wsum[w] = run;
   __syncthreads();
-  int base = 0;
-  for (int q = 0; q < w; q++) base += wsum[q];
-  if (threadIdx.x < (unsigned)E) off[threadIdx.x + 1] = base + run;
+  // what the warps before this one add up to
+  int ahead = lane < w ? wsum[lane] : 0;
+#pragma unroll
+  for (int m = 16; m >= 1; m >>= 1) ahead += __shfl_xor_sync(0xffffffffu, ahead, m);
+  if (threadIdx.x < (unsigned)E) {
+    off[threadIdx.x + 1] = ahead + run;
+    base[threadIdx.x] = ahead + run - padded + before;
+  }
   if (threadIdx.x == 0) off[0] = 0;
   __syncthreads();
   cluster_sync_all();  // every CTA has read the others' totals: they may exit from here on
   if (rank == 0)
     for (int e = threadIdx.x; e <= E; e += blockDim.x) p.offsets[e] = off[e];
-  for (int64_t i0 = lo; i0 < hi; i0 += 32) {
-    const int64_t i = i0 + lane;
-    int e = i < hi ? p.ids[i] : -1;
-    if (e < 0 || e >= E) e = -1;
-    const uint32_t same = __match_any_sync(0xffffffffu, e);
-    int slot = -1;
-    if (e >= 0) slot = off[e] + hw[e] + __popc(same & ((1u << lane) - 1u));
-    __syncwarp();
-    if (e >= 0 && lane == __ffs(same) - 1) hw[e] += __popc(same);
-    __syncwarp();
-    if (i < hi) {
-      p.slots[i] = slot;
-      if (slot >= 0) p.rows[slot] = (int32_t)(i / p.top_k);
+  for (int64_t i0 = lo; i0 < hi; i0 += 32 * kRowsBatch) {
+    int ids[kRowsBatch];
+    load(i0, ids);
+#pragma unroll
+    for (int b = 0; b < kRowsBatch; b++) {
+      const int64_t i = i0 + 32 * b + lane;
+      if (i0 + 32 * b >= hi) break;
+      const int e = ids[b];
+      // lanes of the same expert, one ballot a bit (match.any takes a turn for every
+      // expert in the warp: 300 cycles a step)
+      uint32_t same = 0xFFFFFFFFu;
+#pragma unroll
+      for (int bit = 0; bit < kRowsBits; bit++) {
+        const uint32_t on = __ballot_sync(0xffffffffu, (e >> bit) & 1);
+        same &= (e >> bit) & 1 ? on : ~on;
+      }
+      int at = -1;
+      if (e >= 0) at = base[e] + hw[e] + __popc(same & ((1u << lane) - 1u));
+      __syncwarp();
+      if (e >= 0 && lane == __ffs(same) - 1) hw[e] += __popc(same);
+      __syncwarp();
+      if (i < hi) {
+        p.slots[i] = at;
+        if (at >= 0) p.rows[at] = (int32_t)((uint32_t)i / (uint32_t)p.top_k);
+      }
     }
   }
   // padding rows of the experts, and the rows behind the last one

@@ -960,7 +960,7 @@ sharq_status run_linear_fp4(const sharq_fp4* x, const sharq_fp4* w, const int32_
 
 template <int VPL>
 sharq_status launch_route(const RouteParams& rp, bool bf16, cudaStream_t s) {
-  const size_t smem = rp.groups > 1 ? 4 * (size_t)rp.experts * sizeof(double) : 0;
+  const size_t smem = 4 * (size_t)rp.smem_doubles * sizeof(double);
   const dim3 grid((unsigned)((rp.t + 3) / 4));
   return bf16 ? launch_ex(route_kernel<VPL, true>, grid, dim3(128), smem, s, 1, rp)
               : launch_ex(route_kernel<VPL, false>, grid, dim3(128), smem, s, 1, rp);
@@ -980,6 +980,25 @@ sharq_status check_assignment(int64_t t, int32_t top_k, int32_t experts) {
 int64_t rows_capacity(int64_t t, int32_t top_k, int32_t experts) {
   const int64_t n = t * top_k, reached = n < experts ? n : experts;
   return 128 * (reached + (n - reached) / 128);
+}
+
+int rows_smem(int experts) { return (int)sizeof(int32_t) * ((kRowsWarps + 4) * experts + 1); }
+
+// Whether a cluster of 16 CTAs (beyond the portable 8) of the row-layout kernel fits on this device.
+bool rows_wide_cluster() {
+  static std::atomic<int> known[64];  // by device: 1 no, 2 yes
+  int dev = 0;
+  if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= 64) return false;
+  int k = known[dev].load(std::memory_order_relaxed);
+  if (k == 0) {
+    k = cudaFuncSetAttribute(route_rows_kernel, cudaFuncAttributeNonPortableClusterSizeAllowed, 1) == cudaSuccess &&
+                max_active_clusters(route_rows_kernel, kRowsWarps * 32, (size_t)rows_smem(kMaxExperts), 16) > 0
+            ? 2
+            : 1;
+    (void)cudaGetLastError();
+    known[dev].store(k, std::memory_order_relaxed);
+  }
+  return k == 2;
 }
 
 template <bool YBF16, bool OBF16>
@@ -1450,6 +1469,11 @@ sharq_status sharq_route(const void* logits, sharq_dtype dt, int64_t t, int32_t 
   rp.scale = scale;
   rp.ids = ids;
   rp.weights = weights;
+  rp.smem_doubles = groups > 1 ? experts + 16 : 0;  // in 64 bits, or in 32 with gaps of 32 in all
+  rp.lanes_per_group = 32;
+  while (rp.lanes_per_group * groups > 32) rp.lanes_per_group /= 2;
+  const uint64_t per = (uint64_t)(experts / groups);
+  rp.per_magic = per > 1 ? (uint32_t)(((1ull << 32) + per - 1) / per) : 0;
   cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
   const bool bf16 = dt == SHARQ_BF16;
   if (experts <= 32) return launch_route<1>(rp, bf16, s);
@@ -1486,12 +1510,13 @@ sharq_status sharq_route_rows(const int32_t* ids, int64_t t, int32_t top_k, int3
   rp.capacity = capacity;
   rp.offsets = group_offsets;
   rp.slots = slots;
-  const int max_smem = (int)sizeof(int32_t) * ((kRowsWarps + 3) * kMaxExperts + 1);
-  st = ensure_smem_limit<route_rows_kernel>(max_smem);
+  st = ensure_smem_limit<route_rows_kernel>(rows_smem(kMaxExperts));
   if (st != SHARQ_OK) return st;
   const int64_t want = (rp.n + 1023) / 1024;  // a step of every warp of a CTA takes 1024 ids
-  const unsigned ctas = want >= 8 ? 8 : want >= 4 ? 4 : want >= 2 ? 2 : 1;
-  const size_t smem = sizeof(int32_t) * ((kRowsWarps + 3) * (size_t)experts + 1);
+  const unsigned most = rows_wide_cluster() ? 16 : 8;
+  unsigned ctas = 1;
+  while (ctas < most && 2 * ctas <= want) ctas *= 2;
+  const size_t smem = (size_t)rows_smem(experts);
   return launch_ex(route_rows_kernel, dim3(ctas), dim3(kRowsWarps * 32), smem, reinterpret_cast<cudaStream_t>(stream), ctas, rp);
 }
 
