@@ -375,4 +375,82 @@ __global__ void __launch_bounds__(128) fp4_long_kernel(const Fp4Params p) {
   }
 }
 
+// ------------------------------------------------------ gather of rows
+// FP4 rows laid out again by index.  Every row has its own scales, so this is
+// what quantizing the gathered rows gives, at a quarter of the bytes read and
+// none of the arithmetic for each copy (32768 routed rows of 2048 from 4096
+// tokens: 43 us when every copy was quantized).  A block takes 128 rows, a whole
+// tile of the scale layout, and a part of their columns.
+struct Fp4GatherParams {
+  const uint8_t *s_codes, *s_scales;
+  const float* s_row;
+  uint8_t *d_codes, *d_scales;
+  float* d_row;
+  const int32_t* rows;
+  const int32_t* count;
+  int64_t src_rows, dst_rows;
+  int32_t pieces, blocks;  // 16-byte pieces of a row's codes; 512-byte scale blocks of a row tile
+};
+
+__global__ void __launch_bounds__(256) fp4_gather_kernel(const Fp4GatherParams p) {
+  __shared__ int32_t src[128];
+  grid_dep_wait();
+  grid_dep_launch();
+  const int64_t r0 = (int64_t)blockIdx.x * 128;
+  int64_t end = p.dst_rows;
+  if (p.count) {
+    const int64_t c = (int64_t)__ldg(p.count);
+    end = c < end ? c : end;
+  }
+  if (r0 >= end) return;
+  const int live = (int)(end - r0 < 128 ? end - r0 : 128);
+  for (int i = threadIdx.x; i < 128; i += 256) {
+    int32_t s = i < live ? __ldg(p.rows + r0 + i) : -1;
+    if (s < 0 || s >= p.src_rows) s = -1;
+    src[i] = s;
+    if (blockIdx.y == 0 && i < live) p.d_row[r0 + i] = s >= 0 ? __ldg(p.s_row + s) : 1.0f;  // a zero row's factor is 1
+  }
+  __syncthreads();
+  const int parts = (int)gridDim.y, part = (int)blockIdx.y;
+  // codes: a warp takes a row's share of pieces, lane by lane
+  const int c0 = (int)((int64_t)p.pieces * part / parts), c1 = (int)((int64_t)p.pieces * (part + 1) / parts);
+  const int lane = threadIdx.x & 31, w = threadIdx.x >> 5;
+  for (int c = c0 + lane; c < c1; c += 32) {
+    for (int i0 = w; i0 < live; i0 += 32) {  // four rows' loads in flight
+      uint4 v[4];
+#pragma unroll
+      for (int u = 0; u < 4; u++) {
+        const int i = i0 + 8 * u;
+        const int64_t s = i < live ? src[i] : -1;
+        v[u] = s >= 0 ? __ldg(reinterpret_cast<const uint4*>(p.s_codes) + s * p.pieces + c) : make_uint4(0u, 0u, 0u, 0u);
+      }
+#pragma unroll
+      for (int u = 0; u < 4; u++)
+        if (i0 + 8 * u < live) reinterpret_cast<uint4*>(p.d_codes)[(r0 + i0 + 8 * u) * p.pieces + c] = v[u];
+    }
+  }
+  // scales: 16 bytes of a block are the words of rows q, q + 32, q + 64, q + 96
+  const int b0 = (int)((int64_t)p.blocks * part / parts), b1 = (int)((int64_t)p.blocks * (part + 1) / parts);
+  for (int64_t j = (int64_t)b0 * 32 + threadIdx.x; j < (int64_t)b1 * 32; j += 256) {
+    const int64_t b = j >> 5;
+    const int q = (int)(j & 31);
+    uint32_t v[4];
+#pragma unroll
+    for (int g = 0; g < 4; g++) {
+      const int64_t s = src[q + 32 * g];
+      v[g] = s >= 0 ? __ldg(reinterpret_cast<const uint32_t*>(p.s_scales + ((s >> 7) * p.blocks + b) * 512 + (s & 31) * 16 +
+                                                              ((s >> 5) & 3) * 4))
+                    : 0u;
+    }
+    uint8_t* to = p.d_scales + ((int64_t)blockIdx.x * p.blocks + b) * 512 + q * 16;
+    if (live == 128) {
+      *reinterpret_cast<uint4*>(to) = make_uint4(v[0], v[1], v[2], v[3]);
+    } else {
+#pragma unroll
+      for (int g = 0; g < 4; g++)
+        if (q + 32 * g < live) *reinterpret_cast<uint32_t*>(to + 4 * g) = v[g];
+    }
+  }
+}
+
 }  // namespace sharq

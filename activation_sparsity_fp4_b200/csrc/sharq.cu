@@ -1422,6 +1422,37 @@ sharq_status sharq_quantize_fp4_swiglu(const void* gate, const void* up, sharq_d
   return fp4_dispatch<FRONT_SWIGLU>(fp, out->fmt, dt == SHARQ_BF16, reinterpret_cast<cudaStream_t>(stream));
 }
 
+sharq_status sharq_gather_fp4(const sharq_fp4* src, const int32_t* rows, const int32_t* count, sharq_fp4* dst,
+                              sharq_stream stream) {
+  sharq_status st = check_fp4(src, "source");
+  if (st != SHARQ_OK) return st;
+  st = check_fp4(dst, "destination");
+  if (st != SHARQ_OK) return st;
+  if (src->k != dst->k || src->fmt != dst->fmt)
+    return fail(SHARQ_ERR_INVALID, "source and destination differ in k or format");
+  if (src->experts != 1 || dst->experts != 1) return fail(SHARQ_ERR_INVALID, "rows are gathered from and to experts=1");
+  if (!rows || !aligned(rows, 4) || !aligned(count, 4))
+    return fail(SHARQ_ERR_INVALID, "rows and count must be device int32 arrays");
+  Fp4GatherParams gp;
+  gp.s_codes = static_cast<const uint8_t*>(src->codes);
+  gp.s_scales = static_cast<const uint8_t*>(src->scales);
+  gp.s_row = src->row_scale;
+  gp.d_codes = static_cast<uint8_t*>(dst->codes);
+  gp.d_scales = static_cast<uint8_t*>(dst->scales);
+  gp.d_row = dst->row_scale;
+  gp.rows = rows;
+  gp.count = count;
+  gp.src_rows = src->rows;
+  gp.dst_rows = dst->rows;
+  gp.pieces = (int32_t)(dst->k / 32);
+  gp.blocks = (int32_t)((dst->k / fmt_block(dst->fmt) + 3) / 4);
+  // parts of the columns: eight blocks for every SM where there are columns for it, 512 bytes of a row each at least
+  const int64_t tiles = (dst->rows + 127) / 128, most = (gp.pieces + 31) / 32, want = 8 * (int64_t)sm_count() / tiles + 1;
+  const int64_t parts = want < most ? want : most;
+  return launch_ex(fp4_gather_kernel, dim3((unsigned)tiles, (unsigned)parts), dim3(256), 0,
+                   reinterpret_cast<cudaStream_t>(stream), 1, gp);
+}
+
 sharq_status sharq_linear_fp4(const sharq_fp4* x, const sharq_fp4* w, void* y, sharq_dtype y_dt, sharq_stream stream) {
   return run_linear_fp4(x, w, nullptr, y, y_dt, reinterpret_cast<cudaStream_t>(stream));
 }

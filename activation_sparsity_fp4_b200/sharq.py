@@ -31,7 +31,7 @@ SYMBOLS = ["sharq_weight_sizes", "sharq_prepared_sizes", "sharq_quantize_weight"
            "sharq_linear_paths", "sharq_linear_grouped", "sharq_sync_status", "sharq_selftest_wait_timeout",
            "sharq_last_error", "sharq_launch_count", "sharq_prepare_noalloc", "sharq_prepare_swiglu",
            "sharq_gather_prepared", "sharq_linear_ws", "sharq_linear_workspace_size",
-           "sharq_linear_grouped_gather", "sharq_fp4_sizes", "sharq_quantize_fp4", "sharq_quantize_fp4_swiglu",
+           "sharq_linear_grouped_gather", "sharq_fp4_sizes", "sharq_quantize_fp4", "sharq_quantize_fp4_swiglu", "sharq_gather_fp4",
            "sharq_linear_fp4", "sharq_linear_fp4_grouped", "sharq_route", "sharq_route_rows_capacity",
            "sharq_route_rows", "sharq_combine"]
 NOALLOC_MAX_ROWS = 65536  # SHARQ_NOALLOC_MAX_ROWS of the C header
@@ -97,6 +97,7 @@ def lib() -> ctypes.CDLL:
             "sharq_fp4_sizes": [I64, I64, I32, I, SZ, SZ, SZ],
             "sharq_quantize_fp4": [P, I, I64, I64, P, P, P, F, F, ctypes.POINTER(sharq_fp4), P],
             "sharq_quantize_fp4_swiglu": [P, P, I, I64, P, F, ctypes.POINTER(sharq_fp4), P],
+            "sharq_gather_fp4": [ctypes.POINTER(sharq_fp4), P, P, ctypes.POINTER(sharq_fp4), P],
             "sharq_linear_fp4": [ctypes.POINTER(sharq_fp4), ctypes.POINTER(sharq_fp4), P, I, P],
             "sharq_linear_fp4_grouped": [ctypes.POINTER(sharq_fp4), ctypes.POINTER(sharq_fp4), P, P, I, P],
             "sharq_route": [P, I, I64, I32, I64, P, I, I32, I32, I32, I32, I32, F, P, P, P],
@@ -143,10 +144,11 @@ def _pat(p) -> int:
 
 
 def _dt(d) -> int:
+    v = DTYPES.get(d)
+    if v is not None:
+        return v
     if isinstance(d, torch.dtype):
-        if d not in DTYPES:
-            raise ValueError(f"unsupported dtype {d}")
-        return DTYPES[d]
+        raise ValueError(f"unsupported dtype {d}")
     return int(d)
 
 
@@ -247,6 +249,11 @@ def sharq_quantize_fp4_swiglu(gate_ptr: int, up_ptr: int, dt, stride: int, count
                               stream=None):
     _check(lib().sharq_quantize_fp4_swiglu(gate_ptr, up_ptr, _dt(dt), stride, count_ptr, amax, ctypes.byref(out),
                                            _stream(stream)), "sharq_quantize_fp4_swiglu")
+
+
+def sharq_gather_fp4(src: sharq_fp4, rows_ptr: int, count_ptr, dst: sharq_fp4, stream=None):
+    _check(lib().sharq_gather_fp4(ctypes.byref(src), rows_ptr, count_ptr, ctypes.byref(dst), _stream(stream)),
+           "sharq_gather_fp4")
 
 
 def sharq_linear_fp4(x: sharq_fp4, w: sharq_fp4, y_ptr: int, y_dt, stream=None):
@@ -463,6 +470,10 @@ def _same_device(x: torch.Tensor, *others):
             raise ValueError(f"tensors on {x.device} and {o.device} in one call")
 
 
+def _empty(rows: int, n: int, dtype, x: torch.Tensor) -> torch.Tensor:
+    return torch.empty_strided((rows, n), (n, 1), dtype=dtype, device=x.device)  # (the cheapest of torch's forms)
+
+
 def _rows_of(x: torch.Tensor, what: str) -> torch.Tensor:
     """x as rows of adjacent values whose starts are 16-byte aligned (a copy only where it is not so already)."""
     if x.dim() != 2:
@@ -534,7 +545,9 @@ def quantize_fp4(x: torch.Tensor, fmt, rows: torch.Tensor | None = None, gamma: 
                  out: FP4Matrix | None = None, stream=None) -> FP4Matrix:
     """Rows of x as an FP4 matrix: x (t, k), or (experts, n, k) for a stacked weight.
     rows: int32 indexes of the rows to take (out of range: a zero row).  gamma: RMSNorm
-    in front.  count: one int32 on the GPU; rows from it on are left as they were."""
+    in front.  count: one int32 on the GPU; rows from it on are left as they were.
+    With more rows taken than x has, x is quantized once and its FP4 rows are gathered
+    (`gather_fp4`; the same bits)."""
     if x.dim() not in (2, 3):
         raise ValueError(f"x must be (t, k) or (experts, n, k), has {x.dim()} dimensions")
     _same_device(x, rows, gamma, count)
@@ -551,8 +564,29 @@ def quantize_fp4(x: torch.Tensor, fmt, rows: torch.Tensor | None = None, gamma: 
             count = _i32(count, "count", (1,))
         n_rows = x.shape[-2] if rows is None else rows.numel()
         out = _fp4_out(out, n_rows, x2.shape[1], fmt, experts, x)
+        if rows is not None and n_rows > x2.shape[0]:
+            tokens = FP4Matrix(x2.shape[0], x2.shape[1], fmt, 1, x.device)
+            sharq_quantize_fp4(x2.data_ptr(), x.dtype, x2.shape[0], max(x2.stride(0), x2.shape[1]), None, None,
+                               _ptr(gamma), eps, amax, tokens.struct)
+            sharq_gather_fp4(tokens.struct, rows.data_ptr(), _ptr(count), out.struct)
+            return out
         sharq_quantize_fp4(x2.data_ptr(), x.dtype, x2.shape[0], max(x2.stride(0), x2.shape[1]), _ptr(rows), _ptr(count),
                            _ptr(gamma), eps, amax, out.struct)
+    return out
+
+
+def gather_fp4(src: FP4Matrix, rows: torch.Tensor, count: torch.Tensor | None = None, out: FP4Matrix | None = None,
+               stream=None) -> FP4Matrix:
+    """FP4 rows laid out again: row i of the result is src row rows[i] (int32; out of range: a zero row)."""
+    _same_device(src.buffer, rows, count)
+    with _place(src.buffer, stream):
+        rows = _i32(rows, "rows", (rows.numel(),))
+        if count is not None:
+            count = _i32(count, "count", (1,))
+        out = _fp4_out(out, rows.numel(), src.k, src.fmt, 1, src.buffer)
+        if out is src:
+            raise ValueError("rows cannot be gathered in place")
+        sharq_gather_fp4(src.struct, rows.data_ptr(), _ptr(count), out.struct)
     return out
 
 
@@ -582,7 +616,7 @@ def _aligned(x: torch.Tensor) -> torch.Tensor:
 
 def _product_out(out, rows: int, n: int, dtype, a: FP4Matrix) -> torch.Tensor:
     if out is None:
-        return a.buffer.new_empty((rows, n), dtype=dtype)
+        return _empty(rows, n, dtype, a.buffer)
     if tuple(out.shape) != (rows, n) or not out.is_contiguous() or out.device != a.device:
         raise ValueError(f"out must be a contiguous ({rows}, {n}) tensor on {a.device}")
     return out
@@ -625,8 +659,7 @@ def route(logits: torch.Tensor, top_k: int, score="softmax", bias: torch.Tensor 
             if tuple(bias.shape) != (experts,):
                 raise ValueError(f"bias must have shape ({experts},)")
             bias = bias.float().contiguous()
-        ids = logits.new_empty((t, top_k), dtype=torch.int32)
-        weights = logits.new_empty((t, top_k), dtype=torch.float32)
+        ids, weights = _empty(t, top_k, torch.int32, logits), _empty(t, top_k, torch.float32, logits)
         sharq_route(logits.data_ptr(), logits.dtype, t, experts, max(logits.stride(0), experts), _ptr(bias), score,
                     groups, top_groups, group_top, top_k, renormalize, scale, ids.data_ptr(), weights.data_ptr())
     return ids, weights
@@ -649,8 +682,7 @@ def route_rows(ids: torch.Tensor, experts: int, stream=None) -> RoutedRows:
         ids = _i32(ids, "ids")
         t, top_k = ids.shape
         capacity = sharq_route_rows_capacity(t, top_k, experts)
-        rows, offsets = ids.new_empty((capacity,)), ids.new_empty((experts + 1,))
-        slots = torch.empty_like(ids)
+        rows, offsets, slots = ids.new_empty((capacity,)), ids.new_empty((experts + 1,)), torch.empty_like(ids)
         sharq_route_rows(ids.data_ptr(), t, top_k, experts, rows.data_ptr(), capacity, offsets.data_ptr(),
                          slots.data_ptr())
     return RoutedRows(rows, offsets, slots)
@@ -673,7 +705,7 @@ def combine(y: torch.Tensor, slots: torch.Tensor, weights: torch.Tensor, add: to
                 raise ValueError(f"add must be ({t}, {n}) of y's dtype")
             add = _aligned(add)
         if out is None:
-            out = y.new_empty((t, n), dtype=out_dtype or y.dtype)
+            out = _empty(t, n, out_dtype or y.dtype, y)
         elif tuple(out.shape) != (t, n) or not out.is_contiguous():
             raise ValueError(f"out must be a contiguous ({t}, {n}) tensor")
         y, weights = _aligned(y), weights.contiguous()

@@ -298,7 +298,7 @@ sharq_status sharq_linear_grouped_gather(const sharq_prepared* tokens, const int
  *   sharq_route         logits -> expert ids and weights of every token;
  *   sharq_route_rows    ids -> routed rows, grouped by expert (the `rows` and
  *                       `group_offsets` of every grouped call here);
- *   sharq_quantize_fp4  rows (gathered by `rows`) -> FP4;
+ *   sharq_quantize_fp4  rows (gathered by `rows`) -> FP4, or sharq_gather_fp4 after it;
  *   sharq_linear_fp4_grouped, sharq_quantize_fp4_swiglu, ... the experts;
  *   sharq_combine       the experts' rows -> tokens.
  * They are inference operators, like the rest of the library. */
@@ -351,6 +351,14 @@ sharq_status sharq_quantize_fp4(const void* x, sharq_dtype x_dt, int64_t x_rows,
  * gate/up product need no copy). */
 sharq_status sharq_quantize_fp4_swiglu(const void* gate, const void* up, sharq_dtype dt, int64_t stride,
                                        const int32_t* count, float amax, sharq_fp4* out, sharq_stream stream);
+
+/* FP4 rows laid out again: dst row i is src row rows[i], or a zero row's form if
+ * rows[i] is not in [0, src->rows); count as above.  src and dst share k and format,
+ * experts 1.  Equal to quantizing the gathered rows, bit for bit (a row's form depends
+ * on that row alone): for routed rows, where every token has several copies, quantize
+ * the tokens and gather. */
+sharq_status sharq_gather_fp4(const sharq_fp4* src, const int32_t* rows, const int32_t* count, sharq_fp4* dst,
+                              sharq_stream stream);
 
 /* y[t][n] = sum_j X[t][j] * W[n][j] over the values of two FP4 matrices of one
  * format and k (fp32 accumulation, rounded once to y_dt; as in every fp32 sum, a

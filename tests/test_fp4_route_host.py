@@ -66,6 +66,18 @@ def test_quantize_swiglu_refuses():
         refused(1, q, *ok[:at], bad, *ok[at + 1 :])
 
 
+def test_gather_refuses():
+    f = sharq.sharq_gather_fp4
+    refused(1, f, mat(), 0, None, mat(rows=300), 0)
+    refused(1, f, mat(), 18, None, mat(rows=300), 0)
+    refused(1, f, mat(), 16, 18, mat(rows=300), 0)
+    refused(1, f, mat(), 16, None, mat(k=512), 0)
+    refused(1, f, mat(), 16, None, mat(fmt=0), 0)
+    refused(1, f, mat(experts=2), 16, None, mat(), 0)
+    refused(1, f, mat(), 16, None, mat(experts=2), 0)
+    refused(1, f, mat(), 16, None, mat(rows=0), 0)
+
+
 def test_linear_refuses():
     f = sharq.sharq_linear_fp4
     refused(1, f, mat(), mat(k=512), 16, BF, 0)

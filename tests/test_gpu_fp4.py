@@ -80,6 +80,36 @@ def test_quantize_gathered_rows(cuda_ok, fmt, dtype):
 
 
 @pytest.mark.parametrize("fmt", FMTS)
+@pytest.mark.parametrize("t_dst,k", [(1, 32), (90, 224), (128, 2048), (300, 1056), (700, 8224)])
+def test_gather(cuda_ok, fmt, t_dst, k):
+    """FP4 rows by index are what quantizing the gathered rows gives, at fewer and at more rows than the source has."""
+    x = _rows(k, 150, k)
+    rng = np.random.default_rng(t_dst)
+    rows = rng.integers(0, 150, t_dst).astype(np.int32)
+    rows[rng.random(t_dst) < 0.2] = -1
+    rows[0] = 150
+    if t_dst > 5:
+        rows[[2, 3, 4]] = [149, 149, 2**31 - 1]
+    xr = np.where(((rows >= 0) & (rows < 150))[:, None], x[np.clip(rows, 0, 149)], np.float32(0))
+    want, rd, xd = quantized(xr, fmt), torch.from_numpy(rows).cuda(), to_dev(x, "bf16")
+    src = sharq.quantize_fp4(xd, fmt)
+    _assert_matrix(sharq.gather_fp4(src, rd), want)
+    _assert_matrix(sharq.quantize_fp4(xd, fmt, rows=rd), want)
+    for count in (0, 1, t_dst // 2, t_dst, t_dst + 9):
+        m = sharq.FP4Matrix(t_dst, k, fmt)
+        for part in (m.codes, m.scales):
+            part.fill_(0x22)
+        m.row_scale.fill_(-1.0)
+        sharq.gather_fp4(src, rd, count=torch.tensor([count], dtype=torch.int32).cuda(), out=m)
+        part = [a.copy() for a in want]
+        for a, old in zip(part, (0x22, 2, -1.0)):
+            a[count:] = old
+        _assert_matrix(m, part, zero_pad=False)
+    with pytest.raises(ValueError):
+        sharq.gather_fp4(src, torch.arange(150, dtype=torch.int32).cuda(), out=src)
+
+
+@pytest.mark.parametrize("fmt", FMTS)
 @pytest.mark.parametrize("dtype", ["bf16", "f32"])
 def test_quantize_norm_with_an_exact_factor(cuda_ok, fmt, dtype):
     """Rows of one magnitude 2^a: the mean square is a power of four, the factor exact, and so is every step but gamma's."""
