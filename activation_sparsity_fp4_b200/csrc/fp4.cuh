@@ -141,9 +141,10 @@ struct Fp4Raw {
 };
 
 // Persistent over rows; the next row's loads are issued before the present
-// row's arithmetic, so that both the memory and the issue slots stay busy.
+// row's arithmetic, so that both the memory and the issue slots stay busy.  (Three
+// blocks an SM are asked for where that costs no spills: 32768 x 5120 NVFP4 85 -> 82 us.)
 template <int FMT, int FRONT, bool XBF16, int NJ>
-__global__ void __launch_bounds__(NJ == 1 ? 1024 : 256) fp4_kernel(const Fp4Params p, const int wpr) {
+__global__ void __launch_bounds__(NJ == 1 ? 1024 : 256, NJ == 2 && FRONT == FRONT_NONE ? 3 : 1) fp4_kernel(const Fp4Params p, const int wpr) {
   // [row parity][sum, sum again, largest magnitude][eight for each row of the block, or 32 for its only one]
   __shared__ __align__(16) float red[2][3][64];
   grid_dep_wait();
