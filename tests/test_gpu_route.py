@@ -186,3 +186,32 @@ def test_python_refusals_on_the_gpu(cuda_ok):
                 lambda: sharq.route(y, 2, groups=3)):
         with pytest.raises(sharq.SharqError):
             bad()
+
+
+@pytest.mark.parametrize("score", ["softmax", "sigmoid"])
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32])
+@pytest.mark.parametrize("with_bias,groups,group_top", [(False, 1, 1), (True, 1, 1), (False, 8, 1), (False, 8, 2), (True, 8, 2)])
+def test_many_tokens(cuda_ok, score, dtype, with_bias, groups, group_top):
+    """Enough tokens that neighbours within fp32's error of each other, and equal ones, occur among those that decide:
+    ids equal to a stable sort in 64 bits.  (The scores below are torch's in 64 bits; the kernel's differ from them by
+    a few units of 2^-53, which separates no two that this many draws bring about.)"""
+    t, experts, top_groups, top_k = 20000, 256, 4, 8
+    g = torch.Generator(device="cuda").manual_seed(17)
+    logits = torch.randn((t, experts), generator=g, device="cuda").to(dtype)
+    bias = 0.1 * torch.randn((experts,), generator=g, device="cuda") if with_bias else None
+    ids, w = sharq.route(logits, top_k, score=score, bias=bias, groups=groups, top_groups=top_groups if groups > 1 else 1,
+                         group_top=group_top)
+    z = logits.double()
+    p = torch.softmax(z, 1) if score == "softmax" else 1 / (1 + torch.exp(-z))
+    c = p if bias is None else p + bias.double()
+    by = z if bias is None else c
+    if groups > 1:
+        value = c.view(t, groups, -1).sort(dim=2, descending=True)[0][:, :, :group_top].sum(2)
+        kept = value.sort(dim=1, descending=True, stable=True)[1][:, :top_groups]
+        member = torch.zeros((t, groups), dtype=torch.bool, device="cuda").scatter_(1, kept, True)
+        by = by.masked_fill(~member.repeat_interleave(experts // groups, 1), -float("inf"))
+    want = by.sort(dim=1, descending=True, stable=True)[1][:, :top_k]
+    assert torch.equal(ids.long(), want)
+    ww = p.gather(1, want)
+    ww = ww / ww.sum(1, keepdim=True)
+    assert bool(((w.double() - ww).abs() <= 2 * 27 * 2.0**-24 * ww).all())
