@@ -240,27 +240,36 @@ __global__ void __launch_bounds__(kFp4GemmThreads, 1) gemm_fp4_kernel(const __gr
         if constexpr (kPair) tc_commit_pair_both(smem_u32(bar));
         else tc_commit(bar);
       };
-      for (int tile = cluster; tile < num_tiles && !*abort_flag; tile += nclusters) {
+      // votes, so that the compiler sees one way through the loop
+      auto waited = [&](uint64_t* bar, uint32_t parity) {
+        return __all_sync(0xffffffffu, mbar_wait(bar, parity, p.timeout_ns, abort_flag)) != 0;
+      };
+      for (int tile = cluster; tile < num_tiles; tile += nclusters) {
+        if (__any_sync(0xffffffffu, *abort_flag)) break;
         const TileXY xy = tile_xy(tile, m_tiles, n_tiles, C::kBandTiles);
         if (tile_expert((int64_t)xy.mt * C::BM * CTAS) < 0) continue;
-        if (!mbar_wait(acc_empty, acc_ph, p.timeout_ns, abort_flag)) { give_up(); break; }
+        if (!waited(acc_empty, acc_ph)) { give_up(); break; }
         acc_ph ^= 1u;
         tc_fence_after();
         int left = (int)((p.k + 63) / 64);  // MMAs of this tile still to come (beyond K there are no scales)
-        uint32_t accumulate = 0;
         bool ok = true;
-        for (int kt = 0; kt < k_tiles; kt++) {
-          const uint32_t half = (uint32_t)kt % C::kSfTiles;
-          ok = mbar_wait(&full[stage], ph, p.timeout_ns, abort_flag);
-          if (half == 0) ok = ok && mbar_wait(&sf_ready[slot], sph, p.timeout_ns, abort_flag);
+        // A group's two stages and scales are asked after together: a wait costs the
+        // issuing warp 75 cycles and more though nothing is missing, an MMA 80 of
+        // the 128 that it runs for, so one wait a stage left the pipe idle.
+        for (int kt = 0; ok && kt < k_tiles; kt += C::kSfTiles) {
+          static_assert(C::kSfTiles == 2, "two stages a group");
+          const bool two = kt + 1 < k_tiles, end = kt + C::kSfTiles >= k_tiles;
+          const uint32_t wrap = stage + 1 == C::kStages, stage1 = wrap ? 0u : stage + 1, ph1 = ph ^ wrap;
+          const uint32_t seen = __reduce_and_sync(
+              0xffffffffu, mbar_test3(&full[stage], ph, &sf_ready[slot], sph, &full[stage1], ph1));
+          if ((seen & 3u) != 3u) ok = waited(&full[stage], ph) && waited(&sf_ready[slot], sph);
           if (!ok) break;
           tc_fence_after();
-          const uint32_t ls = lo0 + stage * (uint32_t)(C::kStageBytes >> 4);
           const uint32_t sl = tm + C::BN + slot * (uint32_t)C::kSlotCols;
-          const uint32_t slx = sl + C::cSfx + 4 * C::kChunks * half;
-          const uint32_t slw = sl + C::cSfw + 4 * C::kNRB * C::kChunks * half;
-          const bool last = half == C::kSfTiles - 1 || kt == k_tiles - 1;
-          if (elect_one()) {
+          auto issue = [&](uint32_t st, uint32_t half, int left) {  // the MMAs of a stage
+            const uint32_t ls = lo0 + st * (uint32_t)(C::kStageBytes >> 4);
+            const uint32_t slx = sl + C::cSfx + 4 * C::kChunks * half;
+            const uint32_t slw = sl + C::cSfw + 4 * C::kNRB * C::kChunks * half;
 #pragma unroll
             for (int kb = 0; kb < C::BK / 64; kb++) {
               if (kb < left) {
@@ -271,21 +280,53 @@ __global__ void __launch_bounds__(kFp4GemmThreads, 1) gemm_fp4_kernel(const __gr
                 const uint64_t b = desc_lohi((ls + (C::oW >> 4) + 2 * kb) | kLbo, kHi128);
                 const uint32_t sfa = (slx + 4 * chunk) | (byte << 30);
                 const uint32_t sfb = (slw + 4 * C::kNRB * chunk) | (byte << 30);
-                fp4_mma<KIND, CTAS>(tm, a, b, idesc, sfa, sfb, kb == 0 ? accumulate : 1u);
+                fp4_mma<KIND, CTAS>(tm, a, b, idesc, sfa, sfb, kt > 0 || half > 0 || kb > 0 ? 1u : 0u);
               }
             }
-            commit(&empty[stage]);
-            if (last) commit(&slot_empty[slot]);
-            if (kt == k_tiles - 1) commit(acc_full);
+          };
+          if (two && (seen & 4u)) {  // the usual case: all of the group at once
+            if (elect_one()) {
+              issue(stage, 0, left);
+              commit(&empty[stage]);
+              issue(stage1, 1, left - C::BK / 64);
+              commit(&empty[stage1]);
+              commit(&slot_empty[slot]);
+              if (end) commit(acc_full);
+            }
+            __syncwarp();
+          } else {
+            if (elect_one()) {
+              issue(stage, 0, left);
+              commit(&empty[stage]);
+              if (!two) {
+                commit(&slot_empty[slot]);
+                commit(acc_full);
+              }
+            }
+            __syncwarp();
+            if (two) {
+              ok = waited(&full[stage1], ph1);
+              if (!ok) break;
+              tc_fence_after();
+              if (elect_one()) {
+                issue(stage1, 1, left - C::BK / 64);
+                commit(&empty[stage1]);
+                commit(&slot_empty[slot]);
+                if (end) commit(acc_full);
+              }
+              __syncwarp();
+            }
           }
-          __syncwarp();
-          accumulate = 1;
-          left -= C::BK / 64;
+          left -= C::kSfTiles * (C::BK / 64);
+          if (two) {
+            ph = ph1;
+            stage = stage1;
+          }
           if (++stage == C::kStages) {
             stage = 0;
             ph ^= 1u;
           }
-          if (last && ++slot == C::kSlots) {
+          if (++slot == C::kSlots) {
             slot = 0;
             sph ^= 1u;
           }

@@ -96,6 +96,24 @@ __device__ __forceinline__ bool mbar_try_wait(uint64_t* bar, uint32_t parity) {
   return ok != 0;
 }
 
+// Bits 0 to 2: whether the phases of three barriers have completed; their latencies overlap, and none is waited for.
+__device__ __forceinline__ uint32_t mbar_test3(uint64_t* b0, uint32_t p0, uint64_t* b1, uint32_t p1, uint64_t* b2,
+                                               uint32_t p2) {
+  uint32_t r0, r1, r2;
+  asm volatile(
+      "{\n\t.reg .pred p, q, r;\n\t"
+      "mbarrier.test_wait.parity.shared::cta.b64 p, [%3], %4;\n\t"
+      "mbarrier.test_wait.parity.shared::cta.b64 q, [%5], %6;\n\t"
+      "mbarrier.test_wait.parity.shared::cta.b64 r, [%7], %8;\n\t"
+      "selp.u32 %0, 1, 0, p;\n\t"
+      "selp.u32 %1, 2, 0, q;\n\t"
+      "selp.u32 %2, 4, 0, r;\n\t}"
+      : "=r"(r0), "=r"(r1), "=r"(r2)
+      : "r"(smem_u32(b0)), "r"(p0), "r"(smem_u32(b1)), "r"(p1), "r"(smem_u32(b2)), "r"(p2)
+      : "memory");
+  return r0 | r1 | r2;
+}
+
 // Wait until the phase with the given parity has completed, or until
 // timeout_ns has passed, or until *abort (if given) becomes nonzero.  On a
 // timeout set the error word (unless quiet) and return false.
