@@ -599,9 +599,12 @@ __device__ __forceinline__ void store8(void* base, int64_t at, const float (&v)[
   }
 }
 
-// One thread per 8 columns of a token.
+// One thread per 8 columns of a token; the loads of up to eight places (bf16; four in
+// fp32) are on their way before the first is added.  Bound by DRAM: 4096 tokens x 8 places x
+// 2048 bf16 columns onto a residual, 168 MB.
 template <bool YBF16, bool OBF16>
 __global__ void __launch_bounds__(128) combine_kernel(const CombineParams p) {
+  constexpr int kAhead = YBF16 ? 8 : 4, kWords = YBF16 ? 1 : 2;
   grid_dep_wait();
   grid_dep_launch();
   const int64_t per = p.n / 8;
@@ -610,14 +613,30 @@ __global__ void __launch_bounds__(128) combine_kernel(const CombineParams p) {
   const int64_t tok = g / per, col = (g % per) * 8;
   float acc[8] = {0.0f, 0.0f, 0.0f, 0.0f, 0.0f, 0.0f, 0.0f, 0.0f};
   if (p.add) load8<YBF16>(p.add, tok * p.n + col, acc);
-  for (int j = 0; j < p.top_k; j++) {
-    const int64_t slot = p.slots[tok * p.top_k + j];
-    if (slot < 0 || slot >= p.y_rows) continue;
-    const float wv = p.weights[tok * p.top_k + j];
-    float v[8];
-    load8<YBF16>(p.y, slot * p.n + col, v);
+  const int32_t* slots = p.slots + tok * p.top_k;
+  const float* weights = p.weights + tok * p.top_k;
+  for (int j0 = 0; j0 < p.top_k; j0 += kAhead) {
+    uint4 raw[kAhead][kWords];
+    bool on[kAhead];
 #pragma unroll
-    for (int i = 0; i < 8; i++) acc[i] = __fmaf_rn(wv, v[i], acc[i]);
+    for (int j = 0; j < kAhead; j++) {
+      const int64_t slot = j0 + j < p.top_k ? __ldg(slots + j0 + j) : -1;
+      on[j] = slot >= 0 && slot < p.y_rows;
+      const uint4* from = reinterpret_cast<const uint4*>(static_cast<const uint8_t*>(p.y) +
+                                                         ((on[j] ? slot : 0) * p.n + col) * (YBF16 ? 2 : 4));
+      if (on[j])
+#pragma unroll
+        for (int q = 0; q < kWords; q++) raw[j][q] = __ldg(from + q);
+    }
+#pragma unroll
+    for (int j = 0; j < kAhead; j++) {
+      if (!on[j]) continue;
+      const float wv = __ldg(weights + j0 + j);
+      float v[8];
+      load8<YBF16>(raw[j], 0, v);
+#pragma unroll
+      for (int i = 0; i < 8; i++) acc[i] = __fmaf_rn(wv, v[i], acc[i]);
+    }
   }
   store8<OBF16>(p.out, tok * p.n + col, acc);
 }

@@ -553,6 +553,8 @@ def quantize_fp4(x: torch.Tensor, fmt, rows: torch.Tensor | None = None, gamma: 
     _same_device(x, rows, gamma, count)
     with _place(x, stream):
         experts = x.shape[0] if x.dim() == 3 else 1
+        if experts > 1 and (rows is not None or count is not None):
+            raise ValueError("rows and count go with one matrix, not with a stack")
         x2 = _rows_of(x if x.dim() == 2 else x.flatten(0, 1), "x")
         if gamma is not None:
             if tuple(gamma.shape) != (x2.shape[1],):

@@ -176,6 +176,27 @@ def test_quantize_strides_and_alignment(cuda_ok):
             sharq.quantize_fp4(t, "nvfp4")
 
 
+def test_python_refusals(cuda_ok):
+    x = torch.zeros((4, 64), device="cuda")
+    i32 = torch.zeros(4, dtype=torch.int32, device="cuda")
+    a, w = sharq.quantize_fp4(x, "nvfp4"), sharq.quantize_fp4(torch.zeros((16, 64), device="cuda"), "nvfp4")
+    for bad in (lambda: sharq.quantize_fp4(x[0], "nvfp4"), lambda: sharq.quantize_fp4(x.half(), "nvfp4"),
+                lambda: sharq.quantize_fp4(x, "nvfp4", rows=i32.long()), lambda: sharq.quantize_fp4(x, "nvfp4", rows=i32.cpu()),
+                lambda: sharq.quantize_fp4(x, "nvfp4", gamma=x[0, :32]), lambda: sharq.quantize_fp4(x, "nvfp4", count=i32),
+                lambda: sharq.quantize_fp4(x, "nvfp4", out=w), lambda: sharq.quantize_fp4(x, "mxfp4", out=a),
+                lambda: sharq.quantize_fp4(x.view(2, 2, 64), "nvfp4", rows=i32),
+                lambda: sharq.quantize_fp4_swiglu(x, x[:2], "nvfp4"), lambda: sharq.quantize_fp4_swiglu(x, x.bfloat16(), "nvfp4"),
+                lambda: sharq.linear_fp4(a, w, out=x), lambda: sharq.linear_fp4_grouped(a, w, i32),
+                lambda: sharq.gather_fp4(a, i32.long()), lambda: sharq.linear_fp4(a, w, out_dtype=torch.float16)):
+        with pytest.raises(ValueError):
+            bad()
+    for bad in (lambda: sharq.quantize_fp4(x[:0], "nvfp4"), lambda: sharq.quantize_fp4(x[:, :40], "nvfp4"),
+                lambda: sharq.linear_fp4(w, sharq.quantize_fp4(x, "mxfp4")), lambda: sharq.linear_fp4(w, a),
+                lambda: sharq.linear_fp4(a, sharq.quantize_fp4(torch.zeros((2, 8, 64), device="cuda"), "nvfp4"))):
+        with pytest.raises(sharq.SharqError):
+            bad()
+
+
 def test_bad_rows_stay_by_themselves(cuda_ok):
     """A row with NaN or an infinity has no defined value; the others keep theirs."""
     x = _rows(11, 12, 128)
