@@ -77,6 +77,18 @@ __device__ __forceinline__ float row_reduce(float v, float* red /* wpr floats, a
   return v;
 }
 
+// The row's RMSNorm factor 1 / sqrt(mean + eps), the root's reciprocal rounded once.
+__device__ __forceinline__ float fp4_rstd(float sumsq, int64_t k, float eps) {
+  return __frsqrt_rn(__fadd_rn(__fdiv_rn(sumsq, (float)k), eps));
+}
+
+// NVFP4's second-level scales of a row with the largest magnitude `top` (the rule of tensor_scales).
+__device__ __forceinline__ float fp4_row_enc(float top) {
+  const float g = __fdiv_rn(2688.0f, top);
+  return top > 0.0f ? fminf(g, 3.402823466e38f) : 1.0f;
+}
+__device__ __forceinline__ float fp4_row_dec(float top) { return top > 0.0f ? __fdiv_rn(top, 2688.0f) : 1.0f; }
+
 // Scale code of a block with the largest magnitude a, and the factor onto the E2M1 grid.
 template <int FMT>
 __device__ __forceinline__ uint32_t fp4_scale(float a, float g_enc, float& mul) {
@@ -141,10 +153,12 @@ struct Fp4Raw {
 };
 
 // Persistent over rows; the next row's loads are issued before the present
-// row's arithmetic, so that both the memory and the issue slots stay busy.  (Three
-// blocks an SM are asked for where that costs no spills: 32768 x 5120 NVFP4 85 -> 82 us.)
+// row's arithmetic, so that both the memory and the issue slots stay busy.  32768 x
+// 5120 bf16: MXFP4 66 us (the copy rate), NVFP4 82, behind a norm 103 and 116: issue
+// slots, about 270 instructions for 16 elements of a warp's lanes.  (Asking for a
+// number of resident blocks, even one, had the compiler take more registers: 136.)
 template <int FMT, int FRONT, bool XBF16, int NJ>
-__global__ void __launch_bounds__(NJ == 1 ? 1024 : 256, NJ == 2 && FRONT == FRONT_NONE ? 3 : 1) fp4_kernel(const Fp4Params p, const int wpr) {
+__global__ void __launch_bounds__(NJ == 1 ? 1024 : 256) fp4_kernel(const Fp4Params p, const int wpr) {
   // [row parity][sum, sum again, largest magnitude][eight for each row of the block, or 32 for its only one]
   __shared__ __align__(16) float red[2][3][64];
   grid_dep_wait();
@@ -202,9 +216,9 @@ __global__ void __launch_bounds__(NJ == 1 ? 1024 : 256, NJ == 2 && FRONT == FRON
         for (int j = 0; j < NJ; j++)
 #pragma unroll
           for (int i = 0; i < 16; i++) t = __fmaf_rn(v[j][i] * 0x1p-80f, v[j][i] * 0x1p-80f, t);
-        rs = 0x1p-80f * rstd_from_sumsq(row_reduce<false, NJ == 1>(t, red[par][1] + 8 * group, wr, wpr, bar), p.k, 0.0f);
+        rs = 0x1p-80f * fp4_rstd(row_reduce<false, NJ == 1>(t, red[par][1] + 8 * group, wr, wpr, bar), p.k, 0.0f);
       } else {
-        rs = rstd_from_sumsq(s, p.k, p.eps);
+        rs = fp4_rstd(s, p.k, p.eps);
       }
 #pragma unroll
       for (int j = 0; j < NJ; j++) {
@@ -232,10 +246,9 @@ __global__ void __launch_bounds__(NJ == 1 ? 1024 : 256, NJ == 2 && FRONT == FRON
     }
     float g_enc = 1.0f;
     if constexpr (FMT == FMT_NV) {
-      float g_dec;
       top = p.amax > 0.0f ? p.amax : row_reduce<true, NJ == 1>(top, red[par][2] + 8 * group, wr, wpr, bar);
-      tensor_scales(top, g_enc, g_dec);
-      if (u0 == 0) p.row_scale[r] = g_dec;
+      g_enc = fp4_row_enc(top);
+      if (u0 == 0) p.row_scale[r] = fp4_row_dec(top);
     } else if (u0 == 0) {
       p.row_scale[r] = 1.0f;
     }
@@ -333,7 +346,7 @@ __global__ void __launch_bounds__(128) fp4_long_kernel(const Fp4Params p) {
     };
     const float s = sumsq(1.0f);
     // squares beyond fp32 (values from about 2^64 / sqrt(k) on): again at 2^-80 of their size, where eps is nothing
-    rs = isinf(s) ? __fmul_rn(0x1p-80f, rstd_from_sumsq(sumsq(0x1p-80f), p.k, 0.0f)) : rstd_from_sumsq(s, p.k, p.eps);
+    rs = isinf(s) ? __fmul_rn(0x1p-80f, fp4_rstd(sumsq(0x1p-80f), p.k, 0.0f)) : fp4_rstd(s, p.k, p.eps);
   }
   float g_enc = 1.0f, g_dec = 1.0f;
   if constexpr (FMT == FMT_NV) {
@@ -348,7 +361,8 @@ __global__ void __launch_bounds__(128) fp4_long_kernel(const Fp4Params p) {
       }
       top = block_reduce<true>(top, red);
     }
-    tensor_scales(top, g_enc, g_dec);
+    g_enc = fp4_row_enc(top);
+    g_dec = fp4_row_dec(top);
   }
   if (threadIdx.x == 0) p.row_scale[r] = g_dec;
   const int64_t S = p.k / (FMT == FMT_NV ? 16 : 32);

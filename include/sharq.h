@@ -329,7 +329,7 @@ sharq_status sharq_fp4_sizes(int64_t rows, int64_t k, int32_t experts, sharq_for
                              size_t* scales_bytes, size_t* row_scale_bytes);
 
 /* Quantizes rows of x to FP4:
- *   h = RMSNorm(x) * gamma if gamma != NULL (fp32, as in sharq_prepare), else x;
+ *   h = (x * r) * gamma, r = 1 / sqrt(mean(x^2) + eps), if gamma != NULL, else x;
  *   MXFP4: per 32 elements e = floor(log2 amax) - 2, element = E2M1(h / 2^e);
  *   NVFP4: A = max |h| of the row (or `amax` if > 0), g = 2688 / A, per 16 elements
  *          S = E4M3((amax / 6) * g), element = E2M1(h * (g / S)) (0 if S = 0);
