@@ -454,19 +454,28 @@ def _on(x: torch.Tensor, stream):
         yield
 
 
-_HERE = contextlib.nullcontext()
+class _Here:
+    def __enter__(self):
+        return None
+
+    def __exit__(self, *exc):
+        return None
+
+
+_HERE = _Here()
 
 
 def _place(x: torch.Tensor, stream):
     # the usual call, on the current device's current stream, needs no context at all
-    if stream is None and x.is_cuda and x.get_device() == torch.cuda.current_device():
+    if stream is None and x.is_cuda and x.get_device() == torch._C._cuda_getDevice():
         return _HERE
     return _on(x, stream)
 
 
 def _same_device(x: torch.Tensor, *others):
+    d = x.get_device()
     for o in others:
-        if o is not None and o.get_device() != x.get_device():
+        if o is not None and o.get_device() != d:
             raise ValueError(f"tensors on {x.device} and {o.device} in one call")
 
 
@@ -507,6 +516,8 @@ def _fp4_layout(rows: int, k: int, experts: int, fmt: int) -> tuple[int, int, in
 
 class FP4Matrix:
     """Device buffer of a microscaled FP4 matrix: activations, or a weight of one or ``experts`` stacked blocks."""
+
+    __slots__ = ("rows", "k", "fmt", "experts", "buffer", "struct", "_at", "_end", "__weakref__")
 
     def __init__(self, rows: int, k: int, fmt, experts: int = 1, device="cuda"):
         self.rows, self.k, self.fmt, self.experts = rows, k, _fmt(fmt), experts
