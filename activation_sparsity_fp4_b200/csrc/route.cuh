@@ -191,8 +191,9 @@ __device__ __forceinline__ void sort_desc(uint32_t (&v)[N]) {
 // One warp per token.  Scores are formed in fp32, ranked by redux.sync on their
 // ordered bits, and the ranking is taken where it is certain: neighbours that
 // decide (the top_k and the one after, the groups on either side of the border)
-// further apart than fp32's error, or equal in all that makes them.  A token where they
-// are not is ranked again in 64 bits.  Without a bias the logits themselves are
+// further apart than fp32's error, or equal in all that makes them.  Places taken that
+// are too close to each other are put in order in 64 bits, a lane each; a token where
+// it is open what is taken is ranked again in 64 bits as a whole.  Without a bias the logits themselves are
 // ranked, which is exact.  Error of a score made for ranking: __expf(x) is within
 // 2 + 1.2 |x| units of 2^-23; of that e^x a sigmoid 1 / (1 + e^-l) = s passes on the
 // part 1 - s and adds 1 + 4 units of 2^-24; the softmax adds at most 16 + 5 for its
@@ -242,6 +243,7 @@ __global__ void __launch_bounds__(128, VPL == 16 ? 5 : 10) route_kernel(const Ro
   };
   // no score, fast or not, is further off than this: s (1 - s) (2 + 1.2 |l|) < 0.56 and e^x (2 + 1.2 |x|) <= 2
   const float off = p.softmax ? scale_p * (0x1p-22f + 0x1p-19f) : 0.56f * 0x1p-23f + 0x1p-21f;
+  const float exact_off = p.softmax ? off : 0x1p-22f;  // of score(): expf 2 units of 2^-23, of which s (1 - s) <= 1/4 pass
   uint32_t key[VPL];
   bool unsure = false;
 #pragma unroll
@@ -371,13 +373,14 @@ __global__ void __launch_bounds__(128, VPL == 16 ? 5 : 10) route_kernel(const Ro
   const float ml = my_id >= 0 ? logit(my_id) : -INFINITY;
   float wv = my_id >= 0 ? score(ml) : 0.0f;
   if (p.bias) {
-    // every place against the next one
-    // (the ranking's scores and these, of either place, and the ranking's of an expert behind: four errors)
+    // Every place against the next one: two of these scores among the places taken;
+    // at the border the ranking's too, of the one after and of any behind it.
     const float mb = my_id >= 0 ? __ldg(p.bias + my_id) : 0.0f, mc = wv + mb;
     float nl = __shfl_down_sync(0xffffffffu, ml, 1), nb = __shfl_down_sync(0xffffffffu, mb, 1);
     float nw = __shfl_down_sync(0xffffffffu, wv, 1);
     int ni = __shfl_down_sync(0xffffffffu, my_id, 1);
-    if (lane == p.top_k - 1) {
+    const bool border = lane == p.top_k - 1;
+    if (border) {
       ni = after_id;
       if (ni >= 0) {
         nl = logit(ni);
@@ -385,9 +388,28 @@ __global__ void __launch_bounds__(128, VPL == 16 ? 5 : 10) route_kernel(const Ro
         nw = score(nl);
       }
     }
+    bool order = false;
     if (my_id >= 0 && ni >= 0 && lane < p.top_k) {
       const bool same = ml == nl && mb == nb;
-      if (!same && mc - (nw + nb) <= 4.0f * off + 0x1p-22f * fabsf(mc) && mc < INFINITY) unsure = true;
+      const float gap = mc - (nw + nb), slack = 0x1p-22f * fabsf(mc);
+      if (!same && mc < INFINITY) {
+        if (border || p.softmax) unsure = unsure || gap <= 2.0f * (exact_off + off) + slack;
+        else order = gap <= 2.0f * exact_off + slack;
+      }
+    }
+    if (__any_sync(0xffffffffu, order) && !__any_sync(0xffffffffu, unsure)) {
+      // the right experts, perhaps in the wrong order: a lane's own in 64 bits (sigmoid), and its rank
+      const double cd = my_id >= 0 ? 1.0 / (1.0 + exp(-(double)ml)) + (double)mb : -INFINITY;
+      int rank = 0, from = lane;
+      for (int i = 0; i < p.top_k; i++) {
+        const double oc = __shfl_sync(0xffffffffu, cd, i);
+        const int oi = __shfl_sync(0xffffffffu, my_id, i);
+        rank += oi >= 0 && (oc > cd || (oc == cd && oi < my_id));
+      }
+      for (int i = 0; i < p.top_k; i++)
+        if (__shfl_sync(0xffffffffu, my_id >= 0 ? rank : -1, i) == lane) from = i;
+      my_id = __shfl_sync(0xffffffffu, my_id, from);
+      wv = __shfl_sync(0xffffffffu, wv, from);
     }
   }
   float total = wv;

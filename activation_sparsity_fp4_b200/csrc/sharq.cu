@@ -795,9 +795,12 @@ sharq_status launch_fp4(const Fp4Params& fp, cudaStream_t s) {
   if (fp.k > kFp4MaxHeld)
     return launch_ex(fp4_long_kernel<FMT, FRONT, XBF16>, dim3((unsigned)fp.rows_out), dim3(128), 0, s, 1, fp);
   // Units of 16 a lane: one where every row has an SM to itself and the most lanes finish it soonest (1 x 14336 with
-  // SwiGLU: 4.7 us against 8.3 with four), else two (32768 x 5120 behind a norm: 118 us against 161 with four, whose
-  // registers leave too few warps), four only for rows that eight warps cannot hold otherwise.
-  if (fp.k <= 512 || fp.rows_out <= sm_count()) return launch_fp4_rows<FMT, FRONT, XBF16, 1>(fp, s);
+  // SwiGLU: 5.6 us against 8.3 with four), and for routed rows behind a gate, most of which are padding and cost
+  // their latency alone (14720 rows of 768 for 37 tokens: 17.8 us against 20.8; full rows 35.3 against 33.5); else
+  // two (32768 x 5120 behind a norm: 118 us against 161 with four, whose registers leave too few warps), four only
+  // for rows that eight warps cannot hold otherwise.
+  const bool padded = FRONT == FRONT_SWIGLU && fp.count != nullptr && fp.k <= 4096;
+  if (fp.k <= 512 || fp.rows_out <= sm_count() || padded) return launch_fp4_rows<FMT, FRONT, XBF16, 1>(fp, s);
   if (fp.k <= 8192) return launch_fp4_rows<FMT, FRONT, XBF16, 2>(fp, s);
   return launch_fp4_rows<FMT, FRONT, XBF16, 4>(fp, s);
 }
