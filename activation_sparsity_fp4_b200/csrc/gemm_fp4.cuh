@@ -184,7 +184,7 @@ __global__ void __launch_bounds__(kFp4GemmThreads, 1) gemm_fp4_kernel(const __gr
   // expert of a row tile; -1 = rows outside every group
   auto tile_expert = [&](int64_t m0) -> int {
     if constexpr (kPair) return 0;
-    if (m0 >= (int64_t)__ldg(p.group_offsets + p.experts)) return -1;
+    if (m0 < (int64_t)__ldg(p.group_offsets) || m0 >= (int64_t)__ldg(p.group_offsets + p.experts)) return -1;
     int lo = 0, hi = p.experts;  // off[lo] <= m0 < off[hi]
     while (hi - lo > 1) {
       const int mid = (lo + hi) >> 1;

@@ -294,6 +294,19 @@ def test_grouped(cuda_ok, fmt, counts, n, k):
         assert np.all(got[offsets[-1] :] == -9.0)
 
 
+def test_grouped_rows_in_front_of_the_first_group(cuda_ok):
+    """Offsets need not begin at 0: the rows before them are in no group."""
+    a, b, _ = _grouped_case(60, [300, 200, 100], 136, 288, "nvfp4")
+    offsets = np.array([128, 128, 512, 640], np.int32)
+    y = torch.full((a.rows, 136), -9.0, dtype=torch.float32, device="cuda")
+    sharq.linear_fp4_grouped(a, b, torch.from_numpy(offsets).cuda(), out=y)
+    sharq.sharq_sync_status()
+    xv, wv, got = values(a), values(b).reshape(3, 136, 288), y.cpu().numpy()
+    check_product(got[128:512], xv[128:512], wv[1], False)
+    check_product(got[512:640], xv[512:640], wv[2], False)
+    assert np.all(got[:128] == -9.0) and np.all(got[640:] == -9.0)
+
+
 def test_grouped_clips_the_last_tile(cuda_ok):
     """x->rows need not be whole tiles: the last group ends at the rows there are."""
     a, b, offsets = _grouped_case(50, [100, 200], 72, 64, "nvfp4", extra=-90)
