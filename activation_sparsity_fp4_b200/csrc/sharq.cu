@@ -1399,6 +1399,7 @@ sharq_status sharq_quantize_fp4(const void* x, sharq_dtype x_dt, int64_t x_rows,
   if (!aligned(rows, 4) || !aligned(count, 4)) return fail(SHARQ_ERR_INVALID, "rows and count must be device int32 arrays");
   if (gamma && !aligned(gamma, 16)) return fail(SHARQ_ERR_INVALID, "gamma must be 16-byte aligned");
   if (!(eps >= 0.0f)) return fail(SHARQ_ERR_INVALID, "eps must be >= 0");
+  if (isinf(amax)) return fail(SHARQ_ERR_INVALID, "amax must be finite");
   Fp4Params fp = fp4_params(x, x_rows, x_stride, count, amax, out);
   fp.rows = rows;
   fp.gamma = gamma;
@@ -1420,6 +1421,7 @@ sharq_status sharq_quantize_fp4_swiglu(const void* gate, const void* up, sharq_d
   if (st != SHARQ_OK) return st;
   if (out->experts != 1) return fail(SHARQ_ERR_INVALID, "activations with experts=%d", (int)out->experts);
   if (!aligned(count, 4)) return fail(SHARQ_ERR_INVALID, "count must be a device int32");
+  if (isinf(amax)) return fail(SHARQ_ERR_INVALID, "amax must be finite");
   Fp4Params fp = fp4_params(gate, out->rows, stride, count, amax, out);
   fp.x2 = up;
   return fp4_dispatch<FRONT_SWIGLU>(fp, out->fmt, dt == SHARQ_BF16, reinterpret_cast<cudaStream_t>(stream));
@@ -1436,6 +1438,8 @@ sharq_status sharq_gather_fp4(const sharq_fp4* src, const int32_t* rows, const i
   if (src->experts != 1 || dst->experts != 1) return fail(SHARQ_ERR_INVALID, "rows are gathered from and to experts=1");
   if (!rows || !aligned(rows, 4) || !aligned(count, 4))
     return fail(SHARQ_ERR_INVALID, "rows and count must be device int32 arrays");
+  if (src->codes == dst->codes || src->scales == dst->scales || src->row_scale == dst->row_scale)
+    return fail(SHARQ_ERR_INVALID, "rows cannot be gathered in place");
   Fp4GatherParams gp;
   gp.s_codes = static_cast<const uint8_t*>(src->codes);
   gp.s_scales = static_cast<const uint8_t*>(src->scales);
@@ -1567,6 +1571,7 @@ sharq_status sharq_combine(const void* y, sharq_dtype y_dt, int64_t y_rows, int6
   if (n <= 0 || n % 8 != 0) return fail(SHARQ_ERR_INVALID, "n=%lld must be a positive multiple of 8", (long long)n);
   if (!y || !aligned(y, 16) || !aligned(add, 16) || !out || !aligned(out, 16))
     return fail(SHARQ_ERR_INVALID, "y, add and out must be 16-byte aligned device pointers");
+  if (add == out && y_dt != out_dt) return fail(SHARQ_ERR_INVALID, "out may be add where both have one dtype");
   if (!slots || !aligned(slots, 4) || !weights || !aligned(weights, 4))
     return fail(SHARQ_ERR_INVALID, "slots and weights must be device arrays");
   CombineParams cp;

@@ -450,6 +450,8 @@ def _on(x: torch.Tensor, stream):
         raise ValueError("a CUDA tensor is needed")
     if isinstance(stream, int):
         stream = torch.cuda.ExternalStream(stream, device=x.device)
+    if stream is not None and stream.device != x.device:
+        raise ValueError(f"a stream of {stream.device} for tensors on {x.device}")
     with torch.cuda.device(x.device), torch.cuda.stream(stream):
         yield
 

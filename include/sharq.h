@@ -331,7 +331,7 @@ sharq_status sharq_fp4_sizes(int64_t rows, int64_t k, int32_t experts, sharq_for
 /* Quantizes rows of x to FP4:
  *   h = (x * r) * gamma, r = 1 / sqrt(mean(x^2) + eps), if gamma != NULL, else x;
  *   MXFP4: per 32 elements e = floor(log2 amax) - 2, element = E2M1(h / 2^e);
- *   NVFP4: A = max |h| of the row (or `amax` if > 0), g = 2688 / A, per 16 elements
+ *   NVFP4: A = max |h| of the row (or `amax` if > 0; finite), g = 2688 / A, per 16 elements
  *          S = E4M3((amax / 6) * g), element = E2M1(h * (g / S)) (0 if S = 0);
  * each step rounded once in fp32, E2M1 and E4M3 to nearest even, saturating.
  * x: x_rows rows of k values of dtype x_dt, row r at x + r * x_stride (elements;
@@ -354,7 +354,7 @@ sharq_status sharq_quantize_fp4_swiglu(const void* gate, const void* up, sharq_d
 
 /* FP4 rows laid out again: dst row i is src row rows[i], or a zero row's form if
  * rows[i] is not in [0, src->rows); count as above.  src and dst share k and format,
- * experts 1.  Equal to quantizing the gathered rows, bit for bit (a row's form depends
+ * experts 1, and no memory.  Equal to quantizing the gathered rows, bit for bit (a row's form depends
  * on that row alone): for routed rows, where every token has several copies, quantize
  * the tokens and gather. */
 sharq_status sharq_gather_fp4(const sharq_fp4* src, const int32_t* rows, const int32_t* count, sharq_fp4* dst,
@@ -422,7 +422,7 @@ sharq_status sharq_route_rows(const int32_t* ids, int64_t t, int32_t top_k, int3
  *   out[t] = add[t] + sum_j weights[t][j] * y[slots[t][j]]   (add NULL: 0)
  * in fp32, added in the order of j, rounded once to out_dt.  Places whose slot is
  * outside [0, y_rows) are left out.  y: y_rows * n, add: t * n, both of dtype y_dt;
- * out: t * n (may be add); n a multiple of 8; all 16-byte aligned. */
+ * out: t * n (may be add, of one dtype then); n a multiple of 8; all 16-byte aligned. */
 sharq_status sharq_combine(const void* y, sharq_dtype y_dt, int64_t y_rows, int64_t n, const int32_t* slots,
                            const float* weights, int64_t t, int32_t top_k, const void* add, void* out,
                            sharq_dtype out_dt, sharq_stream stream);

@@ -66,6 +66,36 @@ def test_quantize_swiglu_refuses():
         refused(1, q, *ok[:at], bad, *ok[at + 1 :])
 
 
+def test_amax_must_be_finite():
+    for v in (float("inf"), -float("inf")):
+        refused(1, sharq.sharq_quantize_fp4, 16, BF, 128, 256, None, None, None, 1e-6, v, mat(), 0)
+        refused(1, sharq.sharq_quantize_fp4_swiglu, 16, 16, BF, 512, None, v, mat(), 0)
+
+
+def test_gather_in_place_refuses():
+    refused(1, sharq.sharq_gather_fp4, mat(), 16, None, mat(), 0)
+    a, b = mat(), mat(ptr=32)
+    b.scales = 16
+    refused(1, sharq.sharq_gather_fp4, a, 16, None, b, 0)
+
+
+def test_combine_onto_another_dtype_refuses():
+    refused(1, sharq.sharq_combine, 16, BF, 4, 64, 16, 16, 4, 2, 32, 32, F32, 0)
+    refused(1, sharq.sharq_combine, 16, F32, 4, 64, 16, 16, 4, 2, 32, 32, BF, 0)
+
+
+def test_stream_of_another_device_refuses():
+    class On:  # stands in for a tensor, and for a stream
+        is_cuda = True
+
+        def __init__(self, i):
+            self.device = torch.device("cuda", i)
+
+    with pytest.raises(ValueError, match="stream of cuda:1"):
+        with sharq._place(On(0), On(1)):
+            pass
+
+
 def test_gather_refuses():
     f = sharq.sharq_gather_fp4
     refused(1, f, mat(), 0, None, mat(rows=300), 0)
