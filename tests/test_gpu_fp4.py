@@ -307,6 +307,19 @@ def test_grouped_rows_in_front_of_the_first_group(cuda_ok):
     assert np.all(got[:128] == -9.0) and np.all(got[640:] == -9.0)
 
 
+def test_grouped_many_experts(cuda_ok):
+    """More experts than a block holds the offsets of; a few have rows."""
+    counts = [0] * 1100
+    for e, c in ((3, 130), (1023, 5), (1024, 128), (1099, 40)):
+        counts[e] = c
+    a, b, offsets = _grouped_case(70, counts, 8, 64, "nvfp4")
+    y = sharq.linear_fp4_grouped(a, b, torch.from_numpy(offsets).cuda(), out_dtype=torch.float32)
+    xv, wv, got = values(a), values(b).reshape(1100, 8, 64), y.cpu().numpy()
+    for e in (3, 1023, 1024, 1099):
+        r = slice(int(offsets[e]), int(offsets[e + 1]))
+        check_product(got[r], xv[r], wv[e], False, f"expert {e}")
+
+
 def test_grouped_clips_the_last_tile(cuda_ok):
     """x->rows need not be whole tiles: the last group ends at the rows there are."""
     a, b, offsets = _grouped_case(50, [100, 200], 72, 64, "nvfp4", extra=-90)
