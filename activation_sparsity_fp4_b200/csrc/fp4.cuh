@@ -52,34 +52,88 @@ __device__ __forceinline__ void fp4_load16(const Fp4Params& p, int64_t at, float
 // w * 32 + lane + 32 wpr j of the row), read once.  The row's sum of squares and
 // largest magnitude are reduced by shuffles and, across its warps, through
 // shared memory behind a barrier of those warps alone.
-// WIDE: up to 32 warps a row, else up to 8.
-template <bool MAX, bool WIDE>
-__device__ __forceinline__ float row_reduce(float v, float* red /* wpr floats, a multiple of 8 */, int wr, int wpr,
-                                            int barrier) {
+
+// Largest magnitude.  WIDE: up to 32 warps a row, else up to 8.
+template <bool WIDE>
+__device__ __forceinline__ float row_max(float v, float* red /* wpr floats, a multiple of 8 */, int wr, int wpr,
+                                         int barrier) {
 #pragma unroll
-  for (int m = 16; m >= 1; m >>= 1) {
-    const float o = __shfl_xor_sync(0xffffffffu, v, m);
-    v = MAX ? fmaxf(v, o) : __fadd_rn(v, o);
-  }
+  for (int m = 16; m >= 1; m >>= 1) v = fmaxf(v, __shfl_xor_sync(0xffffffffu, v, m));
   if (wpr > 1) {
     const int lane = threadIdx.x & 31, slots = WIDE ? (wpr + 7) & ~7 : 8;
     if (lane == 0) red[wr] = v;
-    if (wr == 0 && lane >= wpr && lane < slots) red[lane] = 0.0f;  // adds nothing, and no magnitude is smaller
+    if (wr == 0 && lane >= wpr && lane < slots) red[lane] = 0.0f;  // no magnitude is smaller
     asm volatile("bar.sync %0, %1;" ::"r"(barrier), "r"(wpr * 32) : "memory");
     for (int i = 0; i < (WIDE ? slots : 8); i += 8) {
       const float4 c = *reinterpret_cast<const float4*>(red + i), d = *reinterpret_cast<const float4*>(red + i + 4);
-      const float t = MAX ? fmaxf(fmaxf(fmaxf(c.x, c.y), fmaxf(c.z, c.w)), fmaxf(fmaxf(d.x, d.y), fmaxf(d.z, d.w)))
-                          : __fadd_rn(__fadd_rn(__fadd_rn(c.x, c.y), __fadd_rn(c.z, c.w)),
-                                      __fadd_rn(__fadd_rn(d.x, d.y), __fadd_rn(d.z, d.w)));
-      v = i == 0 ? t : (MAX ? fmaxf(v, t) : __fadd_rn(v, t));
+      const float t = fmaxf(fmaxf(fmaxf(c.x, c.y), fmaxf(c.z, c.w)), fmaxf(fmaxf(d.x, d.y), fmaxf(d.z, d.w)));
+      v = i == 0 ? t : fmaxf(v, t);
     }
   }
   return v;
 }
 
-// The row's RMSNorm factor 1 / sqrt(mean + eps), the root's reciprocal rounded once.
+// Sum over a row's units, s[j] that of this lane's unit j.  The order is that of
+// sharq_prepare and of the oracle, a tree of adjacent units whatever warps and lanes
+// hold them, so that a row has one sum in every batch: adjacent lanes first, which
+// gives the sums of chunks of 32 units, then adjacent chunks.  The first shuffles
+// halve the number of sums as they go (a lane keeps those of chunks whose low bits
+// are its own), so two or four units a lane cost no more shuffles than one.
+// LANES: the chunks are added by shuffles again, else by every lane from 16-byte reads.
+// NVFP4 takes the first and MXFP4 the second for the registers that the compiler
+// then needs, which decide between three and four blocks of five warps an SM
+// (32768 x 5120: NVFP4 128 us with 96 registers against 147 with 102, MXFP4 110 with
+// 88 against 124 with 98).
+template <int NJ, bool LANES>
+__device__ __forceinline__ float row_sum(const float (&s)[NJ], float* red /* a float a chunk, a multiple of 8 */, int wr,
+                                         int wpr, int barrier) {
+  static_assert(NJ == 1 || NJ == 2 || NJ == 4, "units a lane");
+  const int lane = threadIdx.x & 31;
+  float a[NJ];
+#pragma unroll
+  for (int j = 0; j < NJ; j++) a[j] = s[j];
+  int m = 1;
+#pragma unroll
+  for (int n = NJ; n > 1; n /= 2, m *= 2)
+#pragma unroll
+    for (int j = 0; j < n; j += 2) {
+      const bool odd = (lane & m) != 0;
+      const float keep = odd ? a[j + 1] : a[j], give = odd ? a[j] : a[j + 1];
+      a[j / 2] = __fadd_rn(keep, __shfl_xor_sync(0xffffffffu, give, m));
+    }
+  float v = a[0];
+#pragma unroll
+  for (int q = NJ; q < 32; q *= 2) v = __fadd_rn(v, __shfl_xor_sync(0xffffffffu, v, q));
+  // lane l: the chunk of units l % NJ of this warp's lanes, chunk wr + wpr (l % NJ) of the row
+  if (wpr == 1) {
+#pragma unroll
+    for (int q = 1; q < NJ; q *= 2) v = __fadd_rn(v, __shfl_xor_sync(0xffffffffu, v, q));
+    return v;
+  }
+  const int slots = (NJ * wpr + 3) & ~3;  // at most 32
+  if (lane < NJ) red[wr + wpr * lane] = v;
+  if (wr == 0 && lane >= NJ * wpr && lane < slots) red[lane] = 0.0f;
+  asm volatile("bar.sync %0, %1;" ::"r"(barrier), "r"(wpr * 32) : "memory");
+  if constexpr (LANES) {
+    v = lane < slots ? red[lane] : 0.0f;
+#pragma unroll
+    for (int q = 1; q < 32; q *= 2) v = __fadd_rn(v, __shfl_xor_sync(0xffffffffu, v, q));
+    return v;
+  }
+  auto four = [&](int i) {
+    const float4 c = *reinterpret_cast<const float4*>(red + i);
+    return __fadd_rn(__fadd_rn(c.x, c.y), __fadd_rn(c.z, c.w));
+  };
+  auto eight = [&](int i) { return slots > i + 4 ? __fadd_rn(four(i), four(i + 4)) : four(i); };
+  v = eight(0);
+  if (slots > 8) v = __fadd_rn(v, eight(8));
+  if (slots > 16) v = __fadd_rn(v, slots > 24 ? __fadd_rn(eight(16), eight(24)) : eight(16));
+  return v;
+}
+
+// 1 / sqrt(mean + eps), every step rounded once as in sharq_prepare (the reciprocal of a root is its quotient).
 __device__ __forceinline__ float fp4_rstd(float sumsq, int64_t k, float eps) {
-  return __frsqrt_rn(__fadd_rn(__fdiv_rn(sumsq, (float)k), eps));
+  return __frcp_rn(__fsqrt_rn(__fadd_rn(__fdiv_rn(sumsq, (float)k), eps)));
 }
 
 // NVFP4's second-level scales of a row with the largest magnitude `top` (the rule of tensor_scales).
@@ -154,18 +208,19 @@ struct Fp4Raw {
 
 // Persistent over rows; the next row's loads are issued before the present
 // row's arithmetic, so that both the memory and the issue slots stay busy.  32768 x
-// 5120 bf16: MXFP4 66 us (the copy rate), NVFP4 82, behind a norm 103 and 116: issue
+// 5120 bf16: MXFP4 66 us (the copy rate), NVFP4 82, behind a norm 107 and 124: issue
 // slots, about 270 instructions for 16 elements of a warp's lanes.  (Asking for a
 // number of resident blocks, even one, had the compiler take more registers: 136.)
 template <int FMT, int FRONT, bool XBF16, int NJ>
 __global__ void __launch_bounds__(NJ == 1 ? 1024 : 256) fp4_kernel(const Fp4Params p, const int wpr) {
-  // [row parity][sum, sum again, largest magnitude][eight for each row of the block, or 32 for its only one]
+  // [row parity][sum, sum again, largest magnitude][a multiple of eight for each row of the block, 32 in all at most]
   __shared__ __align__(16) float red[2][3][64];
   grid_dep_wait();
   grid_dep_launch();
   const int lane = threadIdx.x & 31, w = threadIdx.x >> 5, group = w / wpr, wr = w - group * wpr;
   const int groups = (int)(blockDim.x / (32 * wpr)), bar = 1 + group;
   const int units = (int)(p.k / 16), u0 = wr * 32 + lane, step = 32 * wpr;
+  const int chunks = (NJ * wpr + 7) & ~7;
   int64_t end = p.rows_out;
   if (p.count) {
     const int64_t c = (int64_t)__ldg(p.count);
@@ -198,28 +253,22 @@ __global__ void __launch_bounds__(NJ == 1 ? 1024 : 256) fp4_kernel(const Fp4Para
     fetch(next);
     next = source(r + 2 * stride);
     if constexpr (FRONT == FRONT_NORM) {
-      float lo = 0.0f, hi = 0.0f;
+      auto sumsq = [&](float f, float* buf) {
+        float s[NJ];
 #pragma unroll
-      for (int j = 0; j < NJ; j++)
+        for (int j = 0; j < NJ; j++) {
+          s[j] = 0.0f;
 #pragma unroll
-        for (int i = 0; i < 16; i += 2) {
-          float x = v[j][i], y = v[j][i + 1];
-          fma2(x, y, x, y, lo, hi);
-          lo = x;
-          hi = y;
+          for (int i = 0; i < 16; i++) s[j] = __fmaf_rn(v[j][i] * f, v[j][i] * f, s[j]);
         }
-      const float s = row_reduce<false, NJ == 1>(__fadd_rn(lo, hi), red[par][0] + 8 * group, wr, wpr, bar);
+        return row_sum<NJ, FMT == FMT_NV>(s, buf + chunks * group, wr, wpr, bar);
+      };
+      const float s = sumsq(1.0f, red[par][0]);
       float rs;
-      if (isinf(s)) {  // squares beyond fp32 (from about 2^64 / sqrt(k) on): again at 2^-80 of their size, eps is nothing
-        float t = 0.0f;
-#pragma unroll
-        for (int j = 0; j < NJ; j++)
-#pragma unroll
-          for (int i = 0; i < 16; i++) t = __fmaf_rn(v[j][i] * 0x1p-80f, v[j][i] * 0x1p-80f, t);
-        rs = 0x1p-80f * fp4_rstd(row_reduce<false, NJ == 1>(t, red[par][1] + 8 * group, wr, wpr, bar), p.k, 0.0f);
-      } else {
+      if (isinf(s))  // squares beyond fp32 (from about 2^64 / sqrt(k) on): again at 2^-80 of their size, eps is nothing
+        rs = 0x1p-80f * fp4_rstd(sumsq(0x1p-80f, red[par][1]), p.k, 0.0f);
+      else
         rs = fp4_rstd(s, p.k, p.eps);
-      }
 #pragma unroll
       for (int j = 0; j < NJ; j++) {
         const int u = u0 + step * j;
@@ -246,7 +295,7 @@ __global__ void __launch_bounds__(NJ == 1 ? 1024 : 256) fp4_kernel(const Fp4Para
     }
     float g_enc = 1.0f;
     if constexpr (FMT == FMT_NV) {
-      top = p.amax > 0.0f ? p.amax : row_reduce<true, NJ == 1>(top, red[par][2] + 8 * group, wr, wpr, bar);
+      top = p.amax > 0.0f ? p.amax : row_max<NJ == 1>(top, red[par][2] + 8 * group, wr, wpr, bar);
       g_enc = fp4_row_enc(top);
       if (u0 == 0) p.row_scale[r] = fp4_row_dec(top);
     } else if (u0 == 0) {
