@@ -272,7 +272,7 @@ __global__ void __launch_bounds__(NJ == 1 ? 1024 : 256) fp4_kernel(const Fp4Para
 #pragma unroll
       for (int j = 0; j < NJ; j++) {
         const int u = u0 + step * j;
-        if (u >= units) continue;
+        if (u >= units || isinf(rs)) continue;  // mean and eps 0: a row of zeros stays one
 #pragma unroll
         for (int h = 0; h < 2; h++) {
           float g[8];
@@ -295,7 +295,9 @@ __global__ void __launch_bounds__(NJ == 1 ? 1024 : 256) fp4_kernel(const Fp4Para
     }
     float g_enc = 1.0f;
     if constexpr (FMT == FMT_NV) {
-      top = p.amax > 0.0f ? p.amax : row_max<NJ == 1>(top, red[par][2] + 8 * group, wr, wpr, bar);
+      // with an amax given too, a row that does not exist is one of zeros, as fp4_gather_kernel writes it
+      if (p.amax > 0.0f) top = p.rows && (uint32_t)__ldg(p.rows + r) >= (uint64_t)p.x_rows ? 0.0f : p.amax;
+      else top = row_max<NJ == 1>(top, red[par][2] + 8 * group, wr, wpr, bar);
       g_enc = fp4_row_enc(top);
       if (u0 == 0) p.row_scale[r] = fp4_row_dec(top);
     } else if (u0 == 0) {
@@ -399,7 +401,7 @@ __global__ void __launch_bounds__(128) fp4_long_kernel(const Fp4Params p) {
   }
   float g_enc = 1.0f, g_dec = 1.0f;
   if constexpr (FMT == FMT_NV) {
-    float top = p.amax;
+    float top = src < 0 ? 0.0f : p.amax;
     if (!(top > 0.0f)) {
       top = 0.0f;
       for (int u = threadIdx.x; u < units; u += 128) {

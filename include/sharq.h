@@ -339,8 +339,8 @@ sharq_status sharq_fp4_sizes(int64_t rows, int64_t k, int32_t experts, sharq_for
  * x: x_rows rows of k values of dtype x_dt, row r at x + r * x_stride (elements;
  * >= k, rows 16-byte aligned).  rows == NULL: x_rows must be out->rows *
  * out->experts.  rows != NULL (out->experts 1): DEVICE, out->rows int32 values;
- * row i is quantized from x row rows[i], or from a zero row if rows[i] is not in
- * [0, x_rows).  count: NULL, or a DEVICE int32: rows from *count on (out->experts
+ * row i is quantized from x row rows[i], or is a zero row (codes and scales 0,
+ * factor 1, whatever eps and amax) if rows[i] is not in [0, x_rows).  count: NULL, or a DEVICE int32: rows from *count on (out->experts
  * 1) are left as they were (sharq_route_rows leaves the rows in use in
  * group_offsets[experts]).  A row with NaN or infinities has no defined value;
  * the other rows keep theirs. */

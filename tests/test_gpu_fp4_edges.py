@@ -1,0 +1,44 @@
+"""Plain FP4 rows and products at the ends of their range: rows that do not exist, rows so small or so large that their
+squares, their second-level scale or a product of factors leaves fp32's range."""
+import numpy as np
+import pytest
+import torch
+
+import oracle
+from activation_sparsity_fp4_b200 import sharq
+from fp4_common import check_product, quantized, read_matrix, values
+from gpu_common import to_dev
+
+pytestmark = pytest.mark.gpu
+
+FMTS = ["mxfp4", "nvfp4"]
+
+
+def _same(a, b, what):
+    for name, g, w in zip(("scales", "codes", "row scales"), a, b):
+        assert np.array_equal(g, w), f"{what}: {name} differ"
+
+
+@pytest.mark.parametrize("fmt", FMTS)
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("k", [256, 4096, 8224, 20000])
+@pytest.mark.parametrize("kw", [dict(amax=5.0), dict(gamma=True, eps=0.0), dict(gamma=True, eps=0.0, amax=5.0), {}])
+def test_rows_that_do_not_exist(cuda_ok, fmt, dtype, k, kw):
+    """An index out of range stands for a row of zero codes and scales with the factor 1, whatever amax, gamma or eps,
+    quantized as it is taken and gathered after it alike."""
+    rng = np.random.default_rng(k)
+    x = np.clip(rng.standard_normal((200, k)), -4, 4).astype(np.float32)
+    kw = dict(kw)
+    if kw.pop("gamma", False):
+        kw["gamma"] = to_dev(rng.uniform(0.5, 1.5, k), dtype)
+    xd = to_dev(x, dtype)
+    rows = rng.integers(0, 200, 170).astype(np.int32)
+    rows[[0, 5, 6, 169]] = [-1, 200, 2**31 - 1, -(2**31)]
+    rd = torch.from_numpy(rows).cuda()
+    taken = read_matrix(sharq.quantize_fp4(xd, fmt, rows=rd, **kw))
+    for i in (0, 5, 6, 169):
+        assert not taken[0][i].any() and not taken[1][i].any() and taken[2][i] == 1.0
+    whole = sharq.quantize_fp4(xd, fmt, **kw)
+    _same(read_matrix(sharq.gather_fp4(whole, rd)), taken, "gathered")
+    more = torch.cat([rd, rd])  # more rows than x has: quantized once and gathered
+    _same([a[:170] for a in read_matrix(sharq.quantize_fp4(xd, fmt, rows=more, **kw))], taken, "many rows")
