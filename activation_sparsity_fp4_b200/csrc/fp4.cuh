@@ -131,10 +131,17 @@ __device__ __forceinline__ float row_sum(const float (&s)[NJ], float* red /* a f
   return v;
 }
 
-// 1 / sqrt(mean + eps), every step rounded once as in sharq_prepare (the reciprocal of a root is its quotient).
-__device__ __forceinline__ float fp4_rstd(float sumsq, int64_t k, float eps) {
-  return __frcp_rn(__fsqrt_rn(__fadd_rn(__fdiv_rn(sumsq, (float)k), eps)));
+// mean(x^2) + eps and 1 / sqrt of it, every step rounded once as in sharq_prepare (the reciprocal of a root is its
+// quotient).
+__device__ __forceinline__ float fp4_mean(float sumsq, int64_t k, float eps) {
+  return __fadd_rn(__fdiv_rn(sumsq, (float)k), eps);
 }
+__device__ __forceinline__ float fp4_rstd(float mean) { return __frcp_rn(__fsqrt_rn(mean)); }
+
+// Rows whose squares leave fp32 (values from about 2^64 / sqrt(k) on, or below 2^-45
+// where eps is as small) are summed again at 2^-80 or 2^90 of their size.
+__device__ __forceinline__ bool fp4_mean_in_range(float mean) { return mean >= 0x1p-90f && mean <= 3.402823466e38f; }
+__device__ __forceinline__ float fp4_norm_scale(float mean) { return mean < 1.0f ? 0x1p90f : 0x1p-80f; }
 
 // NVFP4's second-level scales of a row with the largest magnitude `top` (the rule of tensor_scales).
 __device__ __forceinline__ float fp4_row_enc(float top) {
@@ -263,16 +270,18 @@ __global__ void __launch_bounds__(NJ == 1 ? 1024 : 256) fp4_kernel(const Fp4Para
         }
         return row_sum<NJ, FMT == FMT_NV>(s, buf + chunks * group, wr, wpr, bar);
       };
-      const float s = sumsq(1.0f, red[par][0]);
+      const float mean = fp4_mean(sumsq(1.0f, red[par][0]), p.k, p.eps);
       float rs;
-      if (isinf(s))  // squares beyond fp32 (from about 2^64 / sqrt(k) on): again at 2^-80 of their size, eps is nothing
-        rs = 0x1p-80f * fp4_rstd(sumsq(0x1p-80f, red[par][1]), p.k, 0.0f);
-      else
-        rs = fp4_rstd(s, p.k, p.eps);
+      if (fp4_mean_in_range(mean)) {
+        rs = fp4_rstd(mean);
+      } else {
+        const float f = fp4_norm_scale(mean);
+        rs = f * fp4_rstd(fp4_mean(sumsq(f, red[par][1]), p.k, p.eps * f * f));
+      }
 #pragma unroll
       for (int j = 0; j < NJ; j++) {
         const int u = u0 + step * j;
-        if (u >= units || isinf(rs)) continue;  // mean and eps 0: a row of zeros stays one
+        if (u >= units || isinf(rs)) continue;  // r beyond fp32: the row as it is
 #pragma unroll
         for (int h = 0; h < 2; h++) {
           float g[8];
@@ -374,6 +383,7 @@ __global__ void __launch_bounds__(128) fp4_long_kernel(const Fp4Params p) {
     }
     fp4_load16<FRONT, XBF16>(p, off + 16 * (int64_t)u, v);
     if constexpr (FRONT == FRONT_NORM) {
+      if (isinf(rs)) return;  // r beyond fp32: the row as it is
       float g[8];
 #pragma unroll
       for (int h = 0; h < 2; h++) {
@@ -395,9 +405,13 @@ __global__ void __launch_bounds__(128) fp4_long_kernel(const Fp4Params p) {
       }
       return block_reduce<false>(s, red);
     };
-    const float s = sumsq(1.0f);
-    // squares beyond fp32 (values from about 2^64 / sqrt(k) on): again at 2^-80 of their size, where eps is nothing
-    rs = isinf(s) ? __fmul_rn(0x1p-80f, fp4_rstd(sumsq(0x1p-80f), p.k, 0.0f)) : fp4_rstd(s, p.k, p.eps);
+    const float mean = fp4_mean(sumsq(1.0f), p.k, p.eps);
+    if (fp4_mean_in_range(mean)) {
+      rs = fp4_rstd(mean);
+    } else {
+      const float f = fp4_norm_scale(mean);
+      rs = f * fp4_rstd(fp4_mean(sumsq(f), p.k, p.eps * f * f));
+    }
   }
   float g_enc = 1.0f, g_dec = 1.0f;
   if constexpr (FMT == FMT_NV) {

@@ -331,7 +331,8 @@ sharq_status sharq_fp4_sizes(int64_t rows, int64_t k, int32_t experts, sharq_for
 /* Quantizes rows of x to FP4:
  *   h = (x * r) * gamma, r = 1 / sqrt(mean(x^2) + eps), if gamma != NULL, else x
  *       (the squares added as in sharq_prepare: 16 adjacent ones in turn, then a tree of
- *       adjacent sums; for k > 16384 in another order that k alone fixes);
+ *       adjacent sums; for k > 16384 in another order that k alone fixes; squares beyond
+ *       fp32's range on either side are no matter; where r itself is beyond it, h = x);
  *   MXFP4: per 32 elements e = floor(log2 amax) - 2, element = E2M1(h / 2^e);
  *   NVFP4: A = max |h| of the row (or `amax` if > 0; finite), g = 2688 / A, per 16 elements
  *          S = E4M3((amax / 6) * g), element = E2M1(h * (g / S)) (0 if S = 0);

@@ -42,3 +42,21 @@ def test_rows_that_do_not_exist(cuda_ok, fmt, dtype, k, kw):
     _same(read_matrix(sharq.gather_fp4(whole, rd)), taken, "gathered")
     more = torch.cat([rd, rd])  # more rows than x has: quantized once and gathered
     _same([a[:170] for a in read_matrix(sharq.quantize_fp4(xd, fmt, rows=more, **kw))], taken, "many rows")
+
+
+@pytest.mark.parametrize("fmt", FMTS)
+@pytest.mark.parametrize("k", [480, 4096, 8224, 20000])
+@pytest.mark.parametrize("t", [9, 180])
+def test_norm_of_small_and_large_rows(cuda_ok, fmt, k, t):
+    """Without eps a row's normalized form does not depend on its magnitude: rows of 2^e times the first one (exact in
+    fp32, squares up to 2^250 and down to 2^-250) have its bits; a row of zeros is zeros."""
+    rng = np.random.default_rng(k)
+    e = np.array(([0, -40, -60, -70, -90, -110, 70, 120, 0] * 20)[:t])
+    x = (rng.choice([1.0, 1.25, 1.5, -1.0, -1.75], (1, k)) * 2.0 ** e[:, None].astype(np.float64)).astype(np.float32)
+    x[8::9] = 0.0
+    gamma = to_dev(rng.uniform(0.5, 1.5, k), "f32")
+    got = read_matrix(sharq.quantize_fp4(to_dev(x, "f32"), fmt, gamma=gamma, eps=0.0))
+    zero = quantized(np.zeros((1, k), np.float32), fmt)
+    for i in range(t):
+        _same([a[i] for a in got], [a[0] for a in (zero if i % 9 == 8 else got)], f"row {i}, 2^{e[i]}")
+    assert got[1][0].any()
