@@ -143,12 +143,15 @@ __device__ __forceinline__ float fp4_rstd(float mean) { return __frcp_rn(__fsqrt
 __device__ __forceinline__ bool fp4_mean_in_range(float mean) { return mean >= 0x1p-90f && mean <= 3.402823466e38f; }
 __device__ __forceinline__ float fp4_norm_scale(float mean) { return mean < 1.0f ? 0x1p90f : 0x1p-80f; }
 
-// NVFP4's second-level scales of a row with the largest magnitude `top` (the rule of tensor_scales).
+// NVFP4's second-level scales of a row with the largest magnitude `top`: 2688 / top,
+// but at most 2^118, so that neither it nor its quotient by a block's scale (2^-9 at
+// the least) leaves fp32, and what undoes it.
 __device__ __forceinline__ float fp4_row_enc(float top) {
-  const float g = __fdiv_rn(2688.0f, top);
-  return top > 0.0f ? fminf(g, 3.402823466e38f) : 1.0f;
+  return top > 0.0f ? fminf(__fdiv_rn(2688.0f, top), 0x1p118f) : 1.0f;
 }
-__device__ __forceinline__ float fp4_row_dec(float top) { return top > 0.0f ? __fdiv_rn(top, 2688.0f) : 1.0f; }
+__device__ __forceinline__ float fp4_row_dec(float top) {
+  return top > 0.0f ? fmaxf(__fdiv_rn(top, 2688.0f), 0x1p-118f) : 1.0f;
+}
 
 // Scale code of a block with the largest magnitude a, and the factor onto the E2M1 grid.
 template <int FMT>

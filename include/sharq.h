@@ -310,7 +310,8 @@ sharq_status sharq_linear_grouped_gather(const sharq_prepared* tokens, const int
  *              16 NVFP4, 32 MXFP4); the places of a row past its k/b scales are 0,
  *              those of rows past the last one are not written;
  *   row_scale  experts * rows floats: the second-level scale, one for each ROW
- *              (NVFP4: A/2688 with A the row's largest magnitude, MXFP4: 1).  A
+ *              (NVFP4: A/2688 with A the row's largest magnitude, at least
+ *              2^-118; a row of zeros: 1; MXFP4: 1).  A
  *              row's FP4 form then depends on that row alone, not on the batch
  *              it is quantized in, and one pass over the input is enough.
  * Value of element (r, j): E2M1(code) * scale(r, j / b) * row_scale(r).
@@ -334,8 +335,9 @@ sharq_status sharq_fp4_sizes(int64_t rows, int64_t k, int32_t experts, sharq_for
  *       adjacent sums; for k > 16384 in another order that k alone fixes; squares beyond
  *       fp32's range on either side are no matter; where r itself is beyond it, h = x);
  *   MXFP4: per 32 elements e = floor(log2 amax) - 2, element = E2M1(h / 2^e);
- *   NVFP4: A = max |h| of the row (or `amax` if > 0; finite), g = 2688 / A, per 16 elements
- *          S = E4M3((amax / 6) * g), element = E2M1(h * (g / S)) (0 if S = 0);
+ *   NVFP4: A = max |h| of the row (or `amax` if > 0; finite), g = 2688 / A, at most 2^118
+ *          (row_scale is at least 2^-118 then), per 16 elements S = E4M3((amax / 6) * g),
+ *          element = E2M1(h * (g / S)) (0 if S = 0);
  * each step rounded once in fp32, E2M1 and E4M3 to nearest even, saturating.
  * x: x_rows rows of k values of dtype x_dt, row r at x + r * x_stride (elements;
  * >= k, rows 16-byte aligned).  rows == NULL: x_rows must be out->rows *

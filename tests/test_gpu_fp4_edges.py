@@ -60,3 +60,22 @@ def test_norm_of_small_and_large_rows(cuda_ok, fmt, k, t):
     for i in range(t):
         _same([a[i] for a in got], [a[0] for a in (zero if i % 9 == 8 else got)], f"row {i}, 2^{e[i]}")
     assert got[1][0].any()
+
+
+@pytest.mark.parametrize("k", [128, 4096, 20000])
+def test_rows_of_tiny_magnitude(cuda_ok, k):
+    """NVFP4 rows whose 2688 / A leaves fp32: still off by no more than half the widest E2M1 step of a block of scale S
+    (E4M3: within 2^-4 of its value, or 2^-10 below 2^-6), both times the row's factor; zeros stay zeros."""
+    rng = np.random.default_rng(k)
+    e = np.arange(-146, -88, 2)
+    x = (rng.uniform(-1, 1, (len(e), k)) * 2.0 ** e[:, None].astype(np.float64)).astype(np.float32)
+    x[:, :16] *= np.float32(2.0**-8)  # a block whose scale is far below the row's largest
+    x[:, ::5] = 0.0
+    m = sharq.quantize_fp4(to_dev(x, "f32"), "nvfp4")
+    scales, codes, rows = read_matrix(m)
+    S = np.array([oracle.e4m3_decode([c])[0] for c in range(127)], np.float64)[scales]
+    step = (S + 6 * 2.0**-10) * rows.astype(np.float64)[:, None]
+    off = np.abs(values(m) - x.astype(np.float64))
+    bad = np.argwhere(off > np.repeat(step, 16, axis=1) + 2.0**-20 * np.abs(x))
+    assert bad.size == 0, f"row of 2^{e[bad[0][0]]}: off by {off[tuple(bad[0])]}, {len(bad)} values"
+    assert not (codes[x == 0] & 7).any()
