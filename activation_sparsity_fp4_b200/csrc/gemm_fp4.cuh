@@ -68,6 +68,12 @@ struct Fp4GemmParams {
   uint64_t timeout_ns;
 };
 
+// A sum is up to 2^23 k, so that its product with a row factor near fp32's end leaves
+// fp32 where the column's factor would bring it back.  From 2^72 on a factor is taken
+// at 2^-56 of its size, and the output brought up at last (exact, 1 otherwise).  MXFP4's
+// row factors are 1.
+constexpr float kFp4FarRow = 0x1p72f, kFp4FarDown = 0x1p-56f, kFp4FarUp = 0x1p56f;
+
 template <int KIND, int CTAS>
 __device__ __forceinline__ void fp4_mma(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, uint32_t sfa, uint32_t sfb,
                                         uint32_t accumulate) {
@@ -416,14 +422,20 @@ __global__ void __launch_bounds__(kFp4GemmThreads, 1) gemm_fp4_kernel(const __gr
       __syncwarp();
       if (lane == 0) arrive_leader(acc_empty_leader);
       if (row0 >= p.t) continue;
+      auto times = [&](float r, float up) {  // the row factors, read while the tile's MMAs ran
 #pragma unroll
-      for (int c = 0; c < kCols; c += 4) {  // times the row factors, read while the tile's MMAs ran
-        const float4 s = *reinterpret_cast<const float4*>(rws + c);
-        v[c] = __float_as_uint(__fmul_rn(__fmul_rn(__uint_as_float(v[c]), rx), s.x));
-        v[c + 1] = __float_as_uint(__fmul_rn(__fmul_rn(__uint_as_float(v[c + 1]), rx), s.y));
-        v[c + 2] = __float_as_uint(__fmul_rn(__fmul_rn(__uint_as_float(v[c + 2]), rx), s.z));
-        v[c + 3] = __float_as_uint(__fmul_rn(__fmul_rn(__uint_as_float(v[c + 3]), rx), s.w));
-      }
+        for (int c = 0; c < kCols; c += 4) {
+          const float4 s = *reinterpret_cast<const float4*>(rws + c);
+          v[c] = __float_as_uint(__fmul_rn(__fmul_rn(__uint_as_float(v[c]), r), s.x) * up);
+          v[c + 1] = __float_as_uint(__fmul_rn(__fmul_rn(__uint_as_float(v[c + 1]), r), s.y) * up);
+          v[c + 2] = __float_as_uint(__fmul_rn(__fmul_rn(__uint_as_float(v[c + 2]), r), s.z) * up);
+          v[c + 3] = __float_as_uint(__fmul_rn(__fmul_rn(__uint_as_float(v[c + 3]), r), s.w) * up);
+        }
+      };
+      if (KIND == GK_NVF4 && __any_sync(0xffffffffu, rx >= kFp4FarRow))
+        times(rx >= kFp4FarRow ? rx * kFp4FarDown : rx, rx >= kFp4FarRow ? kFp4FarUp : 1.0f);
+      else
+        times(rx, 1.0f);
       if (p.y_bf16) {
 #pragma unroll
         for (int i = 0; i < kCols / 2; i++) {

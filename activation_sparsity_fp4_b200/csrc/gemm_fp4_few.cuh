@@ -231,14 +231,16 @@ __global__ void __launch_bounds__(192, 1) gemm_fp4_few_kernel(const __grid_const
 #pragma unroll
         for (int r = 0; r < kFp4FewMaxSplit; r++)
           if (r < p.split) v[r] = ld_cluster_f32x4(peer[r] + (uint32_t)(t * C::BM * 4));
-        const float rx = __ldg(p.row_x + t0 + t);
+        const float rf = __ldg(p.row_x + t0 + t);
+        const bool far = KIND == GK_NVF4 && rf >= kFp4FarRow;
+        const float rx = far ? rf * kFp4FarDown : rf, up = far ? kFp4FarUp : 1.0f;
         float4 f = v[0];
 #pragma unroll
         for (int r = 1; r < kFp4FewMaxSplit; r++)
           if (r < p.split)
             f = make_float4(__fadd_rn(f.x, v[r].x), __fadd_rn(f.y, v[r].y), __fadd_rn(f.z, v[r].z), __fadd_rn(f.w, v[r].w));
-        f = make_float4(__fmul_rn(__fmul_rn(f.x, rx), rw.x), __fmul_rn(__fmul_rn(f.y, rx), rw.y),
-                        __fmul_rn(__fmul_rn(f.z, rx), rw.z), __fmul_rn(__fmul_rn(f.w, rx), rw.w));
+        f = make_float4(__fmul_rn(__fmul_rn(f.x, rx), rw.x) * up, __fmul_rn(__fmul_rn(f.y, rx), rw.y) * up,
+                        __fmul_rn(__fmul_rn(f.z, rx), rw.z) * up, __fmul_rn(__fmul_rn(f.w, rx), rw.w) * up);
         const int64_t at = (t0 + t) * p.n + n;
         if (p.y_bf16) {
           const __nv_bfloat162 lo = __floats2bfloat162_rn(f.x, f.y), hi = __floats2bfloat162_rn(f.z, f.w);

@@ -79,3 +79,30 @@ def test_rows_of_tiny_magnitude(cuda_ok, k):
     bad = np.argwhere(off > np.repeat(step, 16, axis=1) + 2.0**-20 * np.abs(x))
     assert bad.size == 0, f"row of 2^{e[bad[0][0]]}: off by {off[tuple(bad[0])]}, {len(bad)} values"
     assert not (codes[x == 0] & 7).any()
+
+
+@pytest.mark.parametrize("fmt", FMTS)
+@pytest.mark.parametrize("t,n,k", [(1, 8, 64), (20, 264, 4096), (100, 520, 256), (600, 520, 512)])
+def test_product_of_large_and_small_rows(cuda_ok, fmt, t, n, k):
+    """Factors of rows far apart: every value whose terms stay in range is right."""
+    rng = np.random.default_rng(t)
+    w = rng.standard_normal((n, k)).astype(np.float32)
+    x = rng.standard_normal((t, k)).astype(np.float32)
+    for ex, ew in ((120, -10), (110, -100), (-100, 110), (-80, 80), (122, -60)):
+        a = sharq.quantize_fp4(to_dev(x * np.float32(2.0**ex), "f32"), fmt)
+        b = sharq.quantize_fp4(to_dev(w * np.float32(2.0**ew), "f32"), fmt)
+        xv, wv = values(a), values(b)
+        y = sharq.linear_fp4(a, b, out_dtype=torch.float32)
+        sharq.sharq_sync_status()
+        check_product(y.cpu().numpy(), xv, wv, False, f"2^{ex} x 2^{ew}")
+        assert torch.equal(sharq.linear_fp4(a, b), y.to(torch.bfloat16))
+        offsets = torch.tensor([0, (t + 127) // 128 * 128], dtype=torch.int32).cuda()
+        g = sharq.linear_fp4_grouped(a, b, offsets, out_dtype=torch.float32)
+        check_product(g.cpu().numpy(), xv, wv, False, f"grouped, 2^{ex} x 2^{ew}")
+        # one large row among ordinary ones
+        x1 = x.copy()
+        x1[t // 2] *= np.float32(2.0**120)
+        a = sharq.quantize_fp4(to_dev(x1, "f32"), fmt)
+        c = sharq.quantize_fp4(to_dev(w * np.float32(2.0**-20), "f32"), fmt)
+        for z in (sharq.linear_fp4(a, c, out_dtype=torch.float32), sharq.linear_fp4_grouped(a, c, offsets, out_dtype=torch.float32)):
+            check_product(z.cpu().numpy(), values(a), values(c), False, "one large row")
