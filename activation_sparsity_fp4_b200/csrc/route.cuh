@@ -299,17 +299,27 @@ __global__ void __launch_bounds__(128, VPL == 16 ? 5 : 10) route_kernel(const Ro
         const float ov = __shfl_sync(0xffffffffu, gv, o * lpg);
         before += ov > gv || (ov == gv && o < g);
       }
-      // the border: the last group inside and the first outside
-      const bool head = g < p.groups && sub == 0;
+      // The border.  A group's value is off by its scores' errors and by the rounding
+      // of its terms (each c, and their sum), which may be far larger than it: two of
+      // opposite signs cancel.  It is taken where the least that a group inside may
+      // be worth is above the most that one outside may; a sum beyond fp32 may be
+      // anything.  Without a bias a score is the whole term, off by 110 of 2^-23 of
+      // itself at most (|x| to 88).
+      const bool head = g < p.groups && sub == 0, inside = before < p.top_groups;
+      float err = 0.0f;
+      if (!by_logit) {
+        const float terms = a > -INFINITY ? fabsf(a) + (p.group_top == 2 && b > -INFINITY ? fabsf(b) : 0.0f) : 0.0f;
+        err = (p.bias ? 2.0f * off : fminf(2.0f * off, 0x1p-15f * terms)) + 0x1p-22f * terms + 0x1p-120f;
+      }
       const float in = from_ordered_bits(__reduce_min_sync(
-          0xffffffffu, head && before < p.top_groups ? ordered_bits(gv) : 0xFFFFFFFFu));
+          0xffffffffu, head && inside ? ordered_bits(err < INFINITY ? gv - err : -INFINITY) : 0xFFFFFFFFu));
       const float out = from_ordered_bits(__reduce_max_sync(
-          0xffffffffu, head && before >= p.top_groups ? ordered_bits(gv) : 0u));
-      if (p.top_groups < p.groups && out > -INFINITY && in < INFINITY) {
-        if (by_logit)  // except where even 64 bits may round the scores of different logits to one value
+          0xffffffffu, head && !inside ? ordered_bits(err < INFINITY ? gv + err : INFINITY) : 0u));
+      if (p.top_groups < p.groups && out > -INFINITY) {
+        if (!by_logit)
+          unsure = !(in > out);
+        else if (in < INFINITY)  // except where even 64 bits may round the scores of different logits to one value
           unsure = in != out && (in - out < 0x1p-24f || (p.softmax ? m - in > 700.0f : in > 15.0f || in < -700.0f));
-        else  // two scores on each side; without a bias they are the whole value: off by 110 of 2^-23 of it (|x| to 88)
-          unsure = in - out <= (p.bias ? 4.0f * off : fminf(4.0f * off, 0x1p-14f * in)) + 0x1p-21f * fabsf(in) + 0x1p-120f;
       }
       uint32_t mine = head && before < p.top_groups ? 1u << g : 0u;
       kept = __reduce_or_sync(0xffffffffu, mine);
