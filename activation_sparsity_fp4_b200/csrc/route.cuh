@@ -388,8 +388,13 @@ __global__ void __launch_bounds__(128, VPL == 16 ? 5 : 10) route_kernel(const Ro
   const float ml = my_id >= 0 ? logit(my_id) : -INFINITY;
   float wv = my_id >= 0 ? score(ml) : 0.0f;
   if (p.bias) {
-    // Every place against the next one: two of these scores among the places taken;
-    // at the border the ranking's too, of the one after and of any behind it.
+    // Every place against the next one, by these scores (each within exact_off), and
+    // the last one against the one after.  For an expert z behind that one only the
+    // ranking's scores (within off) say that it is no larger: the two of z and of the
+    // one after more.  And that no place taken is worth less than the last holds by
+    // these scores only while every place is certainly above the next; where one is not
+    // (order), it holds by the ranking's, of that place and of the last: two more.  The
+    // slack is the rounding of c, 2^-24 of it for each score in question.
     const float mb = my_id >= 0 ? __ldg(p.bias + my_id) : 0.0f, mc = wv + mb;
     float nl = __shfl_down_sync(0xffffffffu, ml, 1), nb = __shfl_down_sync(0xffffffffu, mb, 1);
     float nw = __shfl_down_sync(0xffffffffu, wv, 1);
@@ -403,15 +408,17 @@ __global__ void __launch_bounds__(128, VPL == 16 ? 5 : 10) route_kernel(const Ro
         nw = score(nl);
       }
     }
-    bool order = false;
+    bool order = false, near = false;
     if (my_id >= 0 && ni >= 0 && lane < p.top_k) {
       const bool same = ml == nl && mb == nb;
       const float gap = mc - (nw + nb), slack = 0x1p-22f * fabsf(mc);
       if (!same && mc < INFINITY) {
-        if (border || p.softmax) unsure = unsure || gap <= 2.0f * (exact_off + off) + slack;
+        if (border || p.softmax) unsure = unsure || gap <= 2.0f * (exact_off + off) + 1.25f * slack;
         else order = gap <= 2.0f * exact_off + slack;
+        near = border && gap <= 2.0f * exact_off + 4.0f * off + 2.0f * slack;
       }
     }
+    if (__any_sync(0xffffffffu, order) && __any_sync(0xffffffffu, near)) unsure = true;
     if (__any_sync(0xffffffffu, order) && !__any_sync(0xffffffffu, unsure)) {
       // the right experts, perhaps in the wrong order: a lane's own in 64 bits (sigmoid), and its rank
       const double cd = my_id >= 0 ? 1.0 / (1.0 + exp(-(double)ml)) + (double)mb : -INFINITY;

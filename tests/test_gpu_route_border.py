@@ -80,3 +80,17 @@ def test_biases_at_the_ends_of_the_range(cuda_ok):
                     want, ww = routed(z.double().numpy(), top_k, bias=bias.numpy(), **kw)
                     assert np.array_equal(ids.cpu().numpy(), want), (b, kw)
                     assert np.all(np.abs(w.cpu().numpy() - ww) <= 2 * 27 * 2.0**-24 * np.abs(ww) + 1e-37)
+
+
+@pytest.mark.parametrize("spread", [2.0**-24, 2.0**-22, 2.0**-21, 2.0**-20, 2.0**-18])
+def test_places_next_to_each_other_at_the_border(cuda_ok, spread):
+    """A bias that undoes the scores but for a little: places inside in an open order, and the border open too."""
+    g = torch.Generator(device="cuda").manual_seed(5)
+    t, experts = 20000, 48
+    base = torch.randn((experts,), generator=g, device="cuda")
+    z = base + spread * torch.randn((t, experts), generator=g, device="cuda") * 8
+    bias = (0.7 - torch.sigmoid(base.double())).float()
+    for top_k in (1, 2, 8, 31, 32):
+        _check(z, top_k, "sigmoid", bias)
+    p = torch.softmax(base.double(), 0)
+    _check(z, 8, "softmax", (0.7 - p).float())
