@@ -200,7 +200,8 @@ __device__ __forceinline__ void sort_desc(uint32_t (&v)[N]) {
 // 2^-23; of that e^x a sigmoid 1 / (1 + e^-l) = s passes on the part 1 - s and adds
 // 1 + 4 units of 2^-24; the softmax adds at most 16 + 5 for its sum, what the sum's
 // own exponentials are off by (their mean, under 2^-20) and 3 more, 2^-19 in all;
-// the bias 2^-24 of c.  The weights are made with expf.
+// the bias 2^-24 of c.  The weights are formed in fp32, the type they are returned in (expf,
+// their sum, the quotient): off by about 5e-8 where 64 bits rounded once are off by half of that.
 //
 // Bound by ALU issue (the lanes' sort, 19 exchanges at 256 experts, and top_k + 1
 // rounds): 4096 tokens x 128 bf16 4.4 us, 16384 x 256 fp32 12.4 us, with scores, a
@@ -234,7 +235,9 @@ __global__ void __launch_bounds__(128, VPL == 16 ? 5 : 10) route_kernel(const Ro
       sum = 0.0f;
 #pragma unroll
       for (int i = 0; i < VPL; i++) {
-        c[i] = l[i] == m ? 1.0f : (l[i] > -INFINITY ? __expf(l[i] - m) : 0.0f);
+        // not renormalized, the weights are divided by this sum: of the same terms as theirs
+        const float x = l[i] - m;
+        c[i] = l[i] == m ? 1.0f : (l[i] > -INFINITY ? (p.renormalize ? __expf(x) : expf(x)) : 0.0f);
         sum += c[i];
       }
 #pragma unroll

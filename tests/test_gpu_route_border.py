@@ -94,3 +94,19 @@ def test_places_next_to_each_other_at_the_border(cuda_ok, spread):
         _check(z, top_k, "sigmoid", bias)
     p = torch.softmax(base.double(), 0)
     _check(z, 8, "softmax", (0.7 - p).float())
+
+
+def test_weights_that_are_not_renormalized(cuda_ok):
+    """All 32 weights of a softmax add up to 1: the numerators are the terms of the denominator.  One logit of 0 and 31
+    of -c, E = e^-c: the lanes' tree adds equal terms without rounding and rounds 1 + E, 1 + 3E, 1 + 7E, 1 + 15E and
+    1 + 31E, 2^-24 of each; the quotient and the products round by 2^-24 each.  (Numerators and denominator made by
+    different exponentials differ by more.)"""
+    c = torch.linspace(1.0, 8.0, 20000, device="cuda")
+    z = -c[:, None].repeat(1, 32)
+    z[torch.arange(len(c)), torch.arange(len(c)) % 32] = 0.0
+    for bias in (None, torch.linspace(-1, 1, 32, device="cuda")):
+        _, w = sharq.route(z, 32, score="softmax", bias=bias, renormalize=False)
+        e = torch.exp(-c.double())
+        tol = ((5 + 57 * e) / (1 + 31 * e) + 2) * 2.0**-24 * (1 + 2.0**-10)
+        off = (w.double().sum(1) - 1).abs()
+        assert bool((off <= tol).all()), f"{int((off > tol).sum())} tokens, worst {float((off / tol).max())} of the bound"
