@@ -795,11 +795,18 @@ sharq_status launch_fp4(const Fp4Params& fp, cudaStream_t s) {
   if (fp.k > kFp4MaxHeld)
     return launch_ex(fp4_long_kernel<FMT, FRONT, XBF16>, dim3((unsigned)fp.rows_out), dim3(128), 0, s, 1, fp);
   // Units of 16 a lane: one where every row has an SM to itself and the most lanes finish it soonest (1 x 14336 with
-  // SwiGLU: 5.6 us against 8.3 with four), and for routed rows behind a gate, most of which are padding and cost
-  // their latency alone (14720 rows of 768 for 37 tokens: 17.8 us against 20.8; full rows 35.3 against 33.5); else
-  // two (32768 x 5120 behind a norm: 118 us against 161 with four, whose registers leave too few warps), four only
-  // for rows that eight warps cannot hold otherwise.
-  const bool padded = FRONT == FRONT_SWIGLU && fp.count != nullptr && fp.k <= 4096;
+  // SwiGLU: 5.6 us against 8.3 with four); else two (32768 x 5120 behind a norm: 126 us against 161 with four, whose
+  // registers leave too few warps), four only for rows that eight warps cannot hold otherwise.
+  // Routed rows behind a gate (count) are padding to a part that the host does not know, and padding costs its latency
+  // alone, which one unit hides better.  Both sides, one unit / two, us, by rows laid out (rows with values):
+  //   MXFP4 bf16 k 768: 16512 (296) 13.1 / 17.0, 49024 (32768) 69.9 / 72.5; 2048: 26.1 / 30.3, 132 / 137; fp32 alike
+  //   NVFP4 bf16 k 768: 16512 (296) 18.2 / 20.6, 20352 (4096) 25.9 / 25.1, 24448 (8192) 28.6 / 29.7, but 49024 (32768)
+  //     82.8 / 80.9; 2048: 32.5 / 35.4, 41.6 / 45.3, 52.2 / 54.2, but 152 / 148; 5120: 69.1 / 67.2, 102 / 99.7
+  //   NVFP4 fp32, whose one unit spills, k 2048: 53.8 / 48.4, 171 / 160
+  //   where two units leave half a warp's lanes idle, NVFP4 k 1536: bf16 26.5 / 32.8, 120 / 134, fp32 42.8 / 40.8, 137 / 147
+  const bool half_idle = (fp.k / 16 + 31) / 32 % 2 == 1;
+  const bool padded = FRONT == FRONT_SWIGLU && fp.count != nullptr && fp.k <= 4096 &&
+                      (FMT == FMT_MX || (XBF16 && fp.rows_out <= 32768) || half_idle);
   if (fp.k <= 512 || fp.rows_out <= sm_count() || padded) return launch_fp4_rows<FMT, FRONT, XBF16, 1>(fp, s);
   if (fp.k <= 8192) return launch_fp4_rows<FMT, FRONT, XBF16, 2>(fp, s);
   return launch_fp4_rows<FMT, FRONT, XBF16, 4>(fp, s);

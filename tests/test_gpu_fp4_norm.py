@@ -107,3 +107,26 @@ def test_rows_in_turn(cuda_ok, fmt, front, dtype, t, k):
 def test_swiglu_bit_for_bit(cuda_ok, fmt, dtype, t, k):
     x, y = (np.clip(_rows(t + s, t, k, dtype), -60, 60) for s in (0, 1))
     _assert_rows(sharq.quantize_fp4_swiglu(to_dev(x, dtype), to_dev(y, dtype), fmt), quantized(oracle.swiglu(x, y), fmt))
+
+
+@pytest.mark.parametrize("fmt", FMTS)
+@pytest.mark.parametrize("dtype,rows,k", [("bf16", 33000, 256), ("bf16", 33000, 576), ("bf16", 600, 576), ("f32", 600, 576),
+                                          ("f32", 600, 800), ("bf16", 600, 5120)])
+def test_swiglu_of_routed_rows(cuda_ok, fmt, dtype, rows, k):
+    """Mostly padding, with a count, on every side of the rule for units a lane: the form of each row quantized alone."""
+    rng = np.random.default_rng(rows + k)
+    t = 40
+    x, y = (np.clip(_rows(s, t, k, dtype), -60, 60) for s in (0, 1))
+    want = quantized(oracle.swiglu(x, y), fmt)
+    zero = [a[0] for a in quantized(np.zeros((1, k), np.float32), fmt)]
+    pick = np.where(rng.random(rows) < 0.05, rng.integers(0, t, rows), -1)
+    gu = torch.zeros((rows, 2 * k), dtype=torch.bfloat16 if dtype == "bf16" else torch.float32, device="cuda")
+    at = torch.from_numpy(np.flatnonzero(pick >= 0)).cuda()
+    src = torch.from_numpy(pick[pick >= 0]).cuda()
+    gu[at, :k], gu[at, k:] = to_dev(x, dtype)[src], to_dev(y, dtype)[src]
+    n = rows - 100
+    m = sharq.quantize_fp4_swiglu(gu[:, :k], gu[:, k:], fmt, count=torch.tensor([n], dtype=torch.int32).cuda())
+    for got, w, z in zip(read_matrix(m), want, zero):
+        full = np.broadcast_to(z, (rows,) + z.shape).copy()
+        full[pick >= 0] = w[pick[pick >= 0]]
+        assert np.array_equal(got[:n], full[:n])
