@@ -144,8 +144,8 @@ struct GemmParams {
   int64_t t;          // rows of y to store (rows >= t are computed but not stored)
   int64_t t_pad;      // rows of the prepared operands (multiple of 128)
   int64_t n, k;
-  int32_t experts;    // 1 = plain; >1 grouped by group_offsets
-  const int32_t* group_offsets;  // device, experts + 1 (grouped only)
+  int32_t experts;    // stacked weights
+  const int32_t* group_offsets;  // device, experts + 1 (grouped form), else null
   const uint8_t* sf_res;         // tiled, t_pad rows, k/b scales
   const uint8_t* sf_bb;          // tiled, t_pad rows, k/(2b) scales (dense backbone: k/b)
   const uint8_t* sf_w_dense;     // per expert tiled, n rows, k/b
@@ -279,9 +279,9 @@ __global__ void __launch_bounds__(448, 1) gemm_kernel(const __grid_constant__ Ge
 
   // expert of an m tile (grouped form); -1 = rows outside every group
   auto tile_expert = [&](int64_t m0) -> int {
-    if (p.experts <= 1) return 0;
+    if (p.group_offsets == nullptr) return 0;
     int lo = 0, hi = p.experts;  // find e with off[e] <= m0 < off[e+1]
-    if (m0 >= (int64_t)__ldg(p.group_offsets + p.experts)) return -1;
+    if (m0 >= (int64_t)__ldg(p.group_offsets + p.experts) || m0 < (int64_t)__ldg(p.group_offsets)) return -1;
     while (hi - lo > 1) {
       const int mid = (lo + hi) >> 1;
       if ((int64_t)__ldg(p.group_offsets + mid) <= m0) lo = mid;

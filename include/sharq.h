@@ -265,7 +265,7 @@ sharq_status sharq_linear_paths(const sharq_prepared* a, const sharq_weight* w, 
 
 /* Mixture-of-experts form (SharQ evaluates Qwen3-30B-A3B): a holds the routed rows of
  * all experts, grouped by expert; group_offsets (DEVICE, experts+1 int32, non-decreasing,
- * each a multiple of 128, last = a->t rounded up to 128) delimits expert e's rows
+ * each a multiple of 128, last <= a->t rounded up to 128) delimits expert e's rows
  * [off[e], off[e+1]).  w holds w->experts stacked weights.  Rows of y outside every
  * group are left unwritten. */
 sharq_status sharq_linear_grouped(const sharq_prepared* a, const sharq_weight* w, const int32_t* group_offsets,
@@ -280,7 +280,7 @@ sharq_status sharq_linear_grouped(const sharq_prepared* a, const sharq_weight* w
  * The result equals sharq_gather_prepared(tokens, rows) followed by
  * sharq_linear_grouped, bit for bit.
  * rows: DEVICE, routed_rows int32 values; routed_rows a positive multiple of 128;
- * group_offsets as in sharq_linear_grouped, last = routed_rows; y: routed_rows * n.
+ * group_offsets as in sharq_linear_grouped, last <= routed_rows; y: routed_rows * n.
  * Supported: NVFP4 with the 4:8 pair pattern (a padding row is encoded with zero
  * E4M3 scales); other formats and patterns return SHARQ_ERR_UNSUPPORTED.  Index
  * values are not checked on the host. */
@@ -297,7 +297,8 @@ sharq_status sharq_linear_grouped_gather(const sharq_prepared* tokens, const int
  * the host:
  *   sharq_route         logits -> expert ids and weights of every token;
  *   sharq_route_rows    ids -> routed rows, grouped by expert (the `rows` and
- *                       `group_offsets` of every grouped call here);
+ *                       `group_offsets` of every grouped call here, whose arrays may
+ *                       hold more rows than are in use);
  *   sharq_quantize_fp4  rows (gathered by `rows`) -> FP4, or sharq_gather_fp4 after it;
  *   sharq_linear_fp4_grouped, sharq_quantize_fp4_swiglu, ... the experts;
  *   sharq_combine       the experts' rows -> tokens.
