@@ -1405,8 +1405,8 @@ sharq_status sharq_quantize_fp4(const void* x, sharq_dtype x_dt, int64_t x_rows,
   if ((rows || count) && out->experts != 1) return fail(SHARQ_ERR_INVALID, "rows and count need experts=1");
   if (!aligned(rows, 4) || !aligned(count, 4)) return fail(SHARQ_ERR_INVALID, "rows and count must be device int32 arrays");
   if (gamma && !aligned(gamma, 16)) return fail(SHARQ_ERR_INVALID, "gamma must be 16-byte aligned");
-  if (!(eps >= 0.0f)) return fail(SHARQ_ERR_INVALID, "eps must be >= 0");
-  if (isinf(amax)) return fail(SHARQ_ERR_INVALID, "amax must be finite");
+  if (!(eps >= 0.0f) || isinf(eps)) return fail(SHARQ_ERR_INVALID, "eps must be finite and >= 0");
+  if (!isfinite(amax)) return fail(SHARQ_ERR_INVALID, "amax must be finite");
   Fp4Params fp = fp4_params(x, x_rows, x_stride, count, amax, out);
   fp.rows = rows;
   fp.gamma = gamma;
@@ -1428,7 +1428,7 @@ sharq_status sharq_quantize_fp4_swiglu(const void* gate, const void* up, sharq_d
   if (st != SHARQ_OK) return st;
   if (out->experts != 1) return fail(SHARQ_ERR_INVALID, "activations with experts=%d", (int)out->experts);
   if (!aligned(count, 4)) return fail(SHARQ_ERR_INVALID, "count must be a device int32");
-  if (isinf(amax)) return fail(SHARQ_ERR_INVALID, "amax must be finite");
+  if (!isfinite(amax)) return fail(SHARQ_ERR_INVALID, "amax must be finite");
   Fp4Params fp = fp4_params(gate, out->rows, stride, count, amax, out);
   fp.x2 = up;
   return fp4_dispatch<FRONT_SWIGLU>(fp, out->fmt, dt == SHARQ_BF16, reinterpret_cast<cudaStream_t>(stream));

@@ -339,7 +339,8 @@ sharq_status sharq_fp4_sizes(int64_t rows, int64_t k, int32_t experts, sharq_for
  *   NVFP4: A = max |h| of the row (or `amax` if > 0; finite), g = 2688 / A, at most 2^118
  *          (row_scale is at least 2^-118 then), per 16 elements S = E4M3((amax / 6) * g),
  *          element = E2M1(h * (g / S)) (0 if S = 0);
- * each step rounded once in fp32, E2M1 and E4M3 to nearest even, saturating.
+ * each step rounded once in fp32, E2M1 and E4M3 to nearest even, saturating.  eps is
+ * finite and >= 0, amax finite.
  * x: x_rows rows of k values of dtype x_dt, row r at x + r * x_stride (elements;
  * >= k, rows 16-byte aligned).  rows == NULL: x_rows must be out->rows *
  * out->experts.  rows != NULL (out->experts 1): DEVICE, out->rows int32 values;

@@ -72,6 +72,13 @@ def test_amax_must_be_finite():
         refused(1, sharq.sharq_quantize_fp4_swiglu, 16, 16, BF, 512, None, v, mat(), 0)
 
 
+def test_amax_and_eps_that_are_no_numbers():
+    nan, inf = float("nan"), float("inf")
+    refused(1, sharq.sharq_quantize_fp4, 16, BF, 128, 256, None, None, None, 1e-6, nan, mat(), 0)
+    refused(1, sharq.sharq_quantize_fp4_swiglu, 16, 16, BF, 512, None, nan, mat(), 0)
+    refused(1, sharq.sharq_quantize_fp4, 16, BF, 128, 256, None, None, 16, inf, 0.0, mat(), 0)
+
+
 def test_gather_in_place_refuses():
     refused(1, sharq.sharq_gather_fp4, mat(), 16, None, mat(), 0)
     a, b = mat(), mat(ptr=32)
