@@ -763,6 +763,11 @@ sharq_status check_dtype(sharq_dtype dt, const char* what) {
   return SHARQ_OK;
 }
 
+bool overlap(const void* a, size_t a_bytes, const void* b, size_t b_bytes) {
+  const uintptr_t x = reinterpret_cast<uintptr_t>(a), z = reinterpret_cast<uintptr_t>(b);
+  return x < z + b_bytes && z < x + a_bytes;
+}
+
 // Input rows: 16-byte aligned, at least k values apart.
 sharq_status check_rows(const void* x, sharq_dtype dt, int64_t stride, int64_t k, const char* what) {
   if (!x || !aligned(x, 16)) return fail(SHARQ_ERR_INVALID, "%s must be a 16-byte aligned device pointer", what);
@@ -1579,6 +1584,11 @@ sharq_status sharq_combine(const void* y, sharq_dtype y_dt, int64_t y_rows, int6
   if (!y || !aligned(y, 16) || !aligned(add, 16) || !out || !aligned(out, 16))
     return fail(SHARQ_ERR_INVALID, "y, add and out must be 16-byte aligned device pointers");
   if (add == out && y_dt != out_dt) return fail(SHARQ_ERR_INVALID, "out may be add where both have one dtype");
+  // tokens are written while others still read
+  const size_t y_size = y_dt == SHARQ_BF16 ? 2 : 4, out_bytes = (size_t)t * n * (out_dt == SHARQ_BF16 ? 2 : 4);
+  if (overlap(out, out_bytes, y, (size_t)y_rows * n * y_size)) return fail(SHARQ_ERR_INVALID, "out lies in y");
+  if (add && add != out && overlap(out, out_bytes, add, (size_t)t * n * y_size))
+    return fail(SHARQ_ERR_INVALID, "out may be add, not a part of it");
   if (!slots || !aligned(slots, 4) || !weights || !aligned(weights, 4))
     return fail(SHARQ_ERR_INVALID, "slots and weights must be device arrays");
   CombineParams cp;

@@ -429,7 +429,8 @@ sharq_status sharq_route_rows(const int32_t* ids, int64_t t, int32_t top_k, int3
  *   out[t] = add[t] + sum_j weights[t][j] * y[slots[t][j]]   (add NULL: 0)
  * in fp32, added in the order of j, rounded once to out_dt.  Places whose slot is
  * outside [0, y_rows) are left out.  y: y_rows * n, add: t * n, both of dtype y_dt;
- * out: t * n (may be add, of one dtype then); n a multiple of 8; all 16-byte aligned. */
+ * out: t * n (may be add, of one dtype then; no other memory of y or add); n a
+ * multiple of 8; all 16-byte aligned. */
 sharq_status sharq_combine(const void* y, sharq_dtype y_dt, int64_t y_rows, int64_t n, const int32_t* slots,
                            const float* weights, int64_t t, int32_t top_k, const void* add, void* out,
                            sharq_dtype out_dt, sharq_stream stream);

@@ -91,6 +91,17 @@ def test_combine_onto_another_dtype_refuses():
     refused(1, sharq.sharq_combine, 16, F32, 4, 64, 16, 16, 4, 2, 32, 32, BF, 0)
 
 
+def test_combine_onto_its_inputs_refuses():
+    """out may be add and nothing else of what is read: y is 256 x 64 bf16 (32768 bytes), add and out 4 x 64 (512)."""
+    y, add, out = 1 << 20, 1 << 21, 1 << 22
+    args = lambda o, a=None, dt=BF: (y, BF, 256, 64, 16, 16, 4, 8, a, o, dt, 0)
+    for o, dt in ((y, BF), (y + 32768 - 16, BF), (y - 512 + 16, BF), (y - 1024 + 16, F32)):
+        refused(1, sharq.sharq_combine, *args(o, None, dt))
+    for o in (add + 16, add - 16, add + 512 - 16):
+        refused(1, sharq.sharq_combine, *args(o, add))
+    refused(1, sharq.sharq_combine, *args(y, y))
+
+
 def test_stream_of_another_device_refuses():
     class On:  # stands in for a tensor, and for a stream
         is_cuda = True

@@ -215,3 +215,17 @@ def test_many_tokens(cuda_ok, score, dtype, with_bias, groups, group_top):
     ww = p.gather(1, want)
     ww = ww / ww.sum(1, keepdim=True)
     assert bool(((w.double() - ww).abs() <= 2 * 27 * 2.0**-24 * ww).all())
+
+
+def test_combine_beside_its_inputs(cuda_ok):
+    """y, add and out next to each other in one buffer, none of them in another."""
+    buf = torch.randn((30, 64), device="cuda")
+    y, add, out = buf[:20], buf[20:25], buf[25:]
+    slots = torch.arange(10, dtype=torch.int32, device="cuda").view(5, 2)
+    w = torch.rand((5, 2), device="cuda")
+    want = sharq.combine(y.clone(), slots, w, add=add.clone())
+    before = buf[:25].clone()
+    assert torch.equal(sharq.combine(y, slots, w, add=add, out=out), want)
+    assert torch.equal(buf[:25], before)
+    with pytest.raises(sharq.SharqError):
+        sharq.combine(y, slots, w, out=buf[19:24])
