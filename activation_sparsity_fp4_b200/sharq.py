@@ -444,8 +444,9 @@ def linear_grouped_gather(tokens: Prepared, rows: torch.Tensor, w: FP4Weight, of
 
 # ------------------------------------- plain FP4 layers and expert routing
 @contextlib.contextmanager
-def _on(x: torch.Tensor, stream):
-    """Allocate and launch where x lives: its device, and the given stream (default: that device's current one)."""
+def _on(x: torch.Tensor, stream, used):
+    """Allocate and launch where x lives: its device, and the given stream (default: that device's current one).  The
+    memory of the tensors used is not given to other work before that stream is through with them."""
     if not x.is_cuda:
         raise ValueError("a CUDA tensor is needed")
     if isinstance(stream, int):
@@ -453,7 +454,13 @@ def _on(x: torch.Tensor, stream):
     if stream is not None and stream.device != x.device:
         raise ValueError(f"a stream of {stream.device} for tensors on {x.device}")
     with torch.cuda.device(x.device), torch.cuda.stream(stream):
-        yield
+        try:
+            yield
+        finally:
+            if stream is not None:
+                for t in (x, *used):
+                    if t is not None:
+                        (t.buffer if isinstance(t, FP4Matrix) else t).record_stream(stream)
 
 
 class _Here:
@@ -467,11 +474,11 @@ class _Here:
 _HERE = _Here()
 
 
-def _place(x: torch.Tensor, stream):
+def _place(x: torch.Tensor, stream, *used):
     # the usual call, on the current device's current stream, needs no context at all
     if stream is None and x.is_cuda and x.get_device() == torch._C._cuda_getDevice():
         return _HERE
-    return _on(x, stream)
+    return _on(x, stream, used)
 
 
 def _same_device(x: torch.Tensor, *others):
@@ -564,7 +571,7 @@ def quantize_fp4(x: torch.Tensor, fmt, rows: torch.Tensor | None = None, gamma: 
     if x.dim() not in (2, 3):
         raise ValueError(f"x must be (t, k) or (experts, n, k), has {x.dim()} dimensions")
     _same_device(x, rows, gamma, count)
-    with _place(x, stream):
+    with _place(x, stream, rows, gamma, count, out):
         experts = x.shape[0] if x.dim() == 3 else 1
         if experts > 1 and (rows is not None or count is not None):
             raise ValueError("rows and count go with one matrix, not with a stack")
@@ -594,7 +601,7 @@ def gather_fp4(src: FP4Matrix, rows: torch.Tensor, count: torch.Tensor | None = 
                stream=None) -> FP4Matrix:
     """FP4 rows laid out again: row i of the result is src row rows[i] (int32; out of range: a zero row)."""
     _same_device(src.buffer, rows, count)
-    with _place(src.buffer, stream):
+    with _place(src.buffer, stream, rows, count, out):
         rows = _i32(rows, "rows", (rows.numel(),))
         if count is not None:
             count = _i32(count, "count", (1,))
@@ -611,7 +618,7 @@ def quantize_fp4_swiglu(gate: torch.Tensor, up: torch.Tensor, fmt, amax: float =
     if gate.shape != up.shape or gate.dtype != up.dtype:
         raise ValueError("gate and up must have one shape and dtype")
     _same_device(gate, up, count)
-    with _place(gate, stream):
+    with _place(gate, stream, up, count, out):
         gate, up = _rows_of(gate, "gate"), _rows_of(up, "up")
         if gate.stride(0) != up.stride(0):
             gate, up = gate.contiguous(), up.contiguous()
@@ -641,7 +648,7 @@ def linear_fp4(a: FP4Matrix, w: FP4Matrix, out_dtype=torch.bfloat16, out: torch.
                stream=None) -> torch.Tensor:
     """y = a w^T, (rows of a, rows of w)."""
     _same_device(a.buffer, w.buffer)
-    with _place(a.buffer, stream):
+    with _place(a.buffer, stream, w, out):
         out = _product_out(out, a.rows, w.rows, out_dtype, a)
         sharq_linear_fp4(a.struct, w.struct, out.data_ptr(), out.dtype)
     return out
@@ -652,7 +659,7 @@ def linear_fp4_grouped(a: FP4Matrix, w: FP4Matrix, offsets: torch.Tensor, out_dt
     """Rows [offsets[e], offsets[e + 1]) of a times expert e's weight.  Rows outside every
     group are left as they were (undefined in an ``out`` allocated here)."""
     _same_device(a.buffer, w.buffer, offsets)
-    with _place(a.buffer, stream):
+    with _place(a.buffer, stream, w, offsets, out):
         offsets = _i32(offsets, "offsets", (w.experts + 1,))
         out = _product_out(out, a.rows, w.rows, out_dtype, a)
         sharq_linear_fp4_grouped(a.struct, w.struct, offsets.data_ptr(), out.data_ptr(), out.dtype)
@@ -666,7 +673,7 @@ def route(logits: torch.Tensor, top_k: int, score="softmax", bias: torch.Tensor 
     if logits.dim() != 2:
         raise ValueError(f"logits must be (t, experts), has {logits.dim()} dimensions")
     _same_device(logits, bias)
-    with _place(logits, stream):
+    with _place(logits, stream, bias):
         t, experts = logits.shape
         if logits.stride(1) != 1 or logits.stride(0) < experts:
             logits = logits.contiguous()
@@ -709,7 +716,7 @@ def combine(y: torch.Tensor, slots: torch.Tensor, weights: torch.Tensor, add: to
     if y.dim() != 2 or slots.dim() != 2:
         raise ValueError("y must be (rows, n), slots (t, top_k)")
     _same_device(y, slots, weights, add, out)
-    with _place(y, stream):
+    with _place(y, stream, slots, weights, add, out):
         t, top_k = slots.shape
         n = y.shape[1]
         slots = _i32(slots, "slots")
