@@ -218,8 +218,9 @@ struct Fp4Raw {
 
 // Persistent over rows; the next row's loads are issued before the present
 // row's arithmetic, so that both the memory and the issue slots stay busy.  32768 x
-// 5120 bf16: MXFP4 66 us (the copy rate), NVFP4 82, behind a norm 107 and 124: issue
-// slots, about 270 instructions for 16 elements of a warp's lanes.  (Asking for a
+// 5120 bf16: MXFP4 66 us (the copy rate), NVFP4 84, behind a norm 107 and 126: 290
+// instructions for the 16 elements of each of a warp's lanes keep two thirds of the
+// issue slots busy, with the 19 warps an SM that the registers leave.  (Asking for a
 // number of resident blocks, even one, had the compiler take more registers: 136.)
 template <int FMT, int FRONT, bool XBF16, int NJ>
 __global__ void __launch_bounds__(NJ == 1 ? 1024 : 256) fp4_kernel(const Fp4Params p, const int wpr) {
@@ -366,7 +367,9 @@ __device__ __forceinline__ float block_reduce(float v, float* red) {  // 128 thr
 }
 
 // One block of 128 threads per row; a thread takes 16 values at a time and reads
-// them again (from L1 or L2) for each pass over the row.
+// them again (from L1 or L2) for each pass over the row, of which there are up to
+// three.  4096 x 28672 bf16 NVFP4 83 us, behind a norm 111, behind a gate 322 (46, 46
+// and 82 by bytes): the passes' arithmetic.
 template <int FMT, int FRONT, bool XBF16>
 __global__ void __launch_bounds__(128) fp4_long_kernel(const Fp4Params p) {
   __shared__ float red[4];

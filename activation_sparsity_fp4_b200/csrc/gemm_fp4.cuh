@@ -102,10 +102,14 @@ __device__ __forceinline__ void fp4_mma(uint32_t d, uint64_t a, uint64_t b, uint
 // row tiles need not share a weight), CTAS = 2 the plain one (with one CTA a tile it
 // was 398 us where it was 362, and no size was faster).
 //
-// 32768 x 5120 x 5120: NVFP4 330 to 335 us (5.1 PFLOP/s), MXFP4 306 us (5.6), bound by
+// 32768 x 5120 x 5120: NVFP4 328 to 335 us (5.1 PFLOP/s), MXFP4 306 us (5.6), bound by
 // the issue of one warp (about 80 cycles an MMA, with its waits near the 128 that an
 // MMA runs) and by the operands' and scales' way into shared and tensor memory.
-// 40832 routed rows x 1536 x 2048 of 128 experts, NVFP4: 90 us, 400 MB (4.4 TB/s).
+// 2048 x 4096 x 4096: 18.1 us, of which two rounds of tiles are 8.3 us of MMAs and the rest
+// launch, first loads and the last epilogue, which nothing overlaps.
+// 40832 routed rows x 1536 x 2048 of 128 experts, NVFP4: 90 us, 400 MB (4.4 TB/s): the
+// waits for a tile's loads, with three stages in flight (DRAM 53 % busy, the pipe 32 %).
+// NVFP4's instantiations spill 80 bytes a thread at 128 registers, once a tile.
 template <int KIND, int CTAS>
 __global__ void __launch_bounds__(kFp4GemmThreads, 1) gemm_fp4_kernel(const __grid_constant__ Fp4Maps maps, const Fp4GemmParams p) {
   using C = Fp4Cfg<KIND, CTAS>;

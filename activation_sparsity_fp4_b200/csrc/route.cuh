@@ -205,7 +205,8 @@ __device__ __forceinline__ void sort_desc(uint32_t (&v)[N]) {
 //
 // Bound by ALU issue (the lanes' sort, 19 exchanges at 256 experts, and top_k + 1
 // rounds): 4096 tokens x 128 bf16 4.4 us, 16384 x 256 fp32 12.4 us, with scores, a
-// bias and 8 groups 28 to 32 us (all of it in 64 bits: 55 us); one token 2.1 us.
+// bias and 8 groups 28 to 35 us, as many tokens go to 64 bits (all of them: 55 us);
+// one token 2.2 us.
 template <int VPL, bool XBF16>
 __global__ void __launch_bounds__(128, VPL == 16 ? 5 : 10) route_kernel(const RouteParams p) {
   extern __shared__ double route_smem[];  // per warp: the experts' selection values (grouped form)
