@@ -311,10 +311,10 @@ sharq_status sharq_linear_grouped_gather(const sharq_prepared* tokens, const int
  *              16 NVFP4, 32 MXFP4); the places of a row past its k/b scales are 0,
  *              those of rows past the last one are not written;
  *   row_scale  experts * rows floats: the second-level scale, one for each ROW
- *              (NVFP4: A/2688 with A the row's largest magnitude, at least
- *              2^-118; a row of zeros: 1; MXFP4: 1).  A
- *              row's FP4 form then depends on that row alone, not on the batch
- *              it is quantized in, and one pass over the input is enough.
+ *              (NVFP4: A/2688 with A the row's largest magnitude, at least 2^-118, and 1
+ *              for a row of zeros; MXFP4: 1).  A row's FP4 form then depends on that row
+ *              alone, not on the batch it is quantized in, and one pass over the input is
+ *              enough.
  * Value of element (r, j): E2M1(code) * scale(r, j / b) * row_scale(r).
  * Shapes: rows >= 1; k a positive multiple of 32. */
 typedef struct {
@@ -345,10 +345,10 @@ sharq_status sharq_fp4_sizes(int64_t rows, int64_t k, int32_t experts, sharq_for
  * >= k, rows 16-byte aligned).  rows == NULL: x_rows must be out->rows *
  * out->experts.  rows != NULL (out->experts 1): DEVICE, out->rows int32 values;
  * row i is quantized from x row rows[i], or is a zero row (codes and scales 0,
- * factor 1, whatever eps and amax) if rows[i] is not in [0, x_rows).  count: NULL, or a DEVICE int32: rows from *count on (out->experts
- * 1) are left as they were (sharq_route_rows leaves the rows in use in
- * group_offsets[experts]).  A row with NaN or infinities has no defined value;
- * the other rows keep theirs. */
+ * factor 1, whatever eps and amax) if rows[i] is not in [0, x_rows).  count: NULL, or a
+ * DEVICE int32: rows from *count on (out->experts 1) are left as they were
+ * (sharq_route_rows leaves the rows in use in group_offsets[experts]).  A row with NaN
+ * or infinities has no defined value; the other rows keep theirs. */
 sharq_status sharq_quantize_fp4(const void* x, sharq_dtype x_dt, int64_t x_rows, int64_t x_stride,
                                 const int32_t* rows, const int32_t* count, const void* gamma, float eps, float amax,
                                 sharq_fp4* out, sharq_stream stream);
