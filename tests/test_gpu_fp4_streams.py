@@ -50,3 +50,30 @@ def test_inputs_dropped_at_once(cuda_ok, name):
         n = 256 * (900 if "gather" in name else 250)
         want, got = want[:n], got[:n]
     assert torch.equal(got, want)
+
+
+def test_captured_on_a_given_stream(cuda_ok):
+    """The stream of a capture given to the calls, inputs from outside the capture among what they read."""
+    g = torch.Generator(device="cuda").manual_seed(2)
+    x, z = torch.randn((200, 512), generator=g, device="cuda"), torch.randn((200, 16), generator=g, device="cuda")
+    w = sharq.quantize_fp4(torch.randn((16, 256, 512), generator=g, device="cuda"), "nvfp4")
+
+    def layer(s=None):
+        ids, v = sharq.route(z, 4, stream=s)
+        r = sharq.route_rows(ids, 16, stream=s)
+        a = sharq.quantize_fp4(x, "nvfp4", rows=r.rows, count=r.offsets[-1:], stream=s)
+        return sharq.combine(sharq.linear_fp4_grouped(a, w, r.offsets, stream=s), r.slots, v, stream=s)
+
+    layer()
+    torch.cuda.synchronize()
+    side, graph = torch.cuda.Stream(), torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph, stream=side):
+        out = layer(side)
+    for seed in (5, 6):
+        x.copy_(torch.randn((200, 512), generator=g, device="cuda"))
+        z.copy_(torch.randn((200, 16), generator=g, device="cuda"))
+        torch.cuda.synchronize()
+        graph.replay()
+        torch.cuda.synchronize()
+        assert torch.equal(out, layer())
+    del graph
